@@ -56,7 +56,8 @@ typedef enum dsa_status {
 typedef enum dsa_dtype {
   DSA_F32 = 0,
   DSA_BF16 = 1,
-  DSA_E4M3 = 2 /* OCP FP8 E4M3 ("fn": no infinities), used with a per-token f32 scale */
+  DSA_E4M3 = 2, /* OCP FP8 E4M3 ("fn": no infinities), used with a per-token f32 scale */
+  DSA_LATENT_E4M3 = 3 /* quantised latent rows (512 e4m3 codes + 64 bf16), see dsa_paged_cache */
 } dsa_dtype;
 
 /* Bits of the device error word. */
@@ -66,13 +67,22 @@ typedef enum dsa_dtype {
 #define DSA_DEVERR_NAN_SCORE 8     /* NaN indexer score met by the selection */
 #define DSA_DEVERR_TIMEOUT 16      /* a bounded wait inside a kernel gave up */
 #define DSA_DEVERR_QUERY_GROUP 32  /* queries of one group are not in one request */
+#define DSA_DEVERR_SCALE 64        /* scale of a visible quantised latent row is not 2^e, -100 <= e <= 119 */
+#define DSA_DEVERR_NONFINITE 128   /* an infinity or NaN met while quantising */
 
 typedef void* dsa_stream; /* cudaStream_t */
 
 /* A paged per-token cache: `data` is [num_blocks, block_size, dim] of `dtype`, row-major, in
  * device memory, 16-byte aligned, one token per row.  For DSA_E4M3, `scale` is the per-token
  * dequantisation scale [num_blocks, block_size] f32 (value = code * scale, scale > 0); it is
- * NULL for the other dtypes.  block_size is 64. */
+ * NULL for the other dtypes.  block_size is 64.
+ *
+ * DSA_LATENT_E4M3 is the quantised form of the 576-wide latent rows (dim is 576: 512 latent + 64
+ * RoPE).  `data` is [num_blocks, 64, 640] bytes: 512 e4m3 codes, then the 64 RoPE elements in
+ * bf16; `scale` is [num_blocks, 64, 4] f32, 16-byte aligned: element i < 512 of a row has the value
+ * code[i] * scale[i / 128].  A scale is a power of two, 2^e with -100 <= e <= 119, so every value
+ * is exact in bf16 and the attention kernels multiply by the very values the cache stands for.
+ * A row takes 656 bytes instead of 1152. */
 typedef struct dsa_paged_cache {
   const void* data;
   const float* scale;
@@ -181,14 +191,15 @@ size_t dsa_indexer_topk_workspace_size(int32_t num_queries);
  * then k >= max_context is required (k bounds the rows per query).  A caller whose queries all
  * see at most K positions skips the indexer and the selection and calls this directly.
  * q: device [num_queries, H, d_v + d_rope] of q_dtype; latent: paged cache with
- * dim == d_v + d_rope and dtype == q_dtype (f32 or bf16); idx: device int32 [num_queries, k]
- * or NULL (dense);
+ * dim == d_v + d_rope and dtype == q_dtype (f32 or bf16), or DSA_LATENT_E4M3 (d_v 512, d_rope 64;
+ * a selected row with a bad scale sets DSA_DEVERR_SCALE and is skipped); idx: device int32
+ * [num_queries, k] or NULL (dense);
  * out: device [num_queries, H, d_v] of q_dtype; lse: device f32 [num_queries, H] or NULL.
  * workspace: device scratch of at least dsa_mla_workspace_size(num_queries, H, d_v, k) bytes,
  * 256-byte aligned (may be NULL when that size is 0).
  * The decode entry point splits each query's k rows across CTAs and merges the partial
  * results (log-sum-exp combine); the prefill entry point gives each query whole CTAs.
- * Fast path: H == 128, d_v == 512, d_rope == 64, bf16.
+ * Fast path: H == 128 or 64, d_v == 512, d_rope == 64, bf16; with a quantised cache any H <= 128.
  */
 dsa_status dsa_sparse_mla_decode(const void* q, int32_t q_dtype, int32_t H, int32_t d_v,
                                  int32_t d_rope, const dsa_paged_cache* latent,
@@ -227,6 +238,85 @@ dsa_status dsa_sparse_mla_decode_noalloc(const void* q, int32_t q_dtype, int32_t
 
 /* Bytes of workspace dsa_sparse_mla_decode needs for these sizes (0 when none). Host only. */
 size_t dsa_mla_workspace_size(int32_t num_queries, int32_t H, int32_t d_v, int32_t k);
+
+/* Chunks of new tokens of several requests, side by side in rows 0 .. num_tokens-1 of a tensor:
+ * request r has the rows cu_tokens[r] .. cu_tokens[r+1]-1 (device int32 [num_reqs + 1],
+ * non-decreasing; a request may have none) and seq_len[r] tokens in its cache once the chunk is in
+ * it (device int32 [num_reqs]), so its n rows sit at the positions seq_len[r]-n .. seq_len[r]-1.
+ * Rows from cu_tokens[num_reqs] on belong to no request (a padded batch): inputs there are not
+ * read, outputs are left as they are.  block_table: device int32 [num_reqs, max_blocks];
+ * max_context: host bound, every seq_len[r] <= max_context <= max_blocks * 64.
+ * A row whose request has cu_tokens or seq_len outside these bounds sets DSA_DEVERR_REQUEST and is
+ * treated as a row behind the last one.  The arrays are read on the device: a captured call
+ * follows their values at each replay. */
+typedef struct dsa_chunks {
+  int32_t num_tokens;
+  int32_t num_reqs;
+  const int32_t* cu_tokens;
+  const int32_t* seq_len;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  int32_t max_context;
+} dsa_chunks;
+
+/*
+ * Writes the new tokens' rows into the paged caches the other calls read (the caches' `data` and
+ * `scale` are written here), quantising as it writes where the cache is quantised.
+ *   k:  device [num_tokens, keys->dim] indexer keys, row t at k + t * k_stride elements, or NULL
+ *       with keys NULL;
+ *   kv: device [num_tokens, latent->dim] latent rows, row t at kv + t * kv_stride elements, or
+ *       NULL with latent NULL.
+ * x_dtype: DSA_F32 or DSA_BF16, of both inputs.  keys: DSA_F32, DSA_BF16 or DSA_E4M3; latent: DSA_F32,
+ * DSA_BF16 or DSA_LATENT_E4M3; block_size 64.  Unquantised caches take the values (rounded once to
+ * bf16 from f32 inputs).  A quantised group of elements (a whole key row; 128 latent elements) gets
+ * the scale 2^e with the smallest e such that |x| <= 448 * 2^e for all of it, -100 <= e <= 119 (1
+ * for a group of zeros), and the codes nearest to x / 2^e (ties to even, saturating).  An infinity
+ * or NaN in a quantised group sets DSA_DEVERR_NONFINITE and is stored as NaN; it does not enter
+ * the group's scale.  RoPE elements are stored as given.
+ * Every row is written by one warp; two tokens of one call in one slot (only block tables that
+ * share a block that is being written can cause it) leave a mixture of the two rows there.
+ */
+dsa_status dsa_cache_append(const void* k, int64_t k_stride, const void* kv, int64_t kv_stride,
+                            int32_t x_dtype, const dsa_paged_cache* keys,
+                            const dsa_paged_cache* latent, const dsa_chunks* chunks,
+                            dsa_stream stream);
+
+/*
+ * Reads cached rows back: out[t] = the values of the row at token t's position (the inverse of
+ * dsa_cache_append; with seq_len[r] tokens as request r's chunk the whole request is read).
+ * cache: any dtype; out: device [num_tokens, cache->dim] of out_dtype (DSA_F32 or DSA_BF16).  bf16
+ * output of an e4m3 key cache or an f32 cache is rounded once; of the others it is exact.
+ * A block id outside the pool sets DSA_DEVERR_BLOCK_ID and leaves the row of out as it is.
+ */
+dsa_status dsa_cache_read(const dsa_paged_cache* cache, const dsa_chunks* chunks, void* out,
+                          int32_t out_dtype, dsa_stream stream);
+
+/*
+ * Dense MLA in MQA mode of chunks of new tokens over the paged latent cache (the tokens' own rows are
+ * in the cache already): the token at position p attends to the positions 0..p of its request.
+ *   logit_s = softmax_scale * (q[t,h,:] . row(s)),   s = 0 .. p
+ *   out[t,h,:] = sum_s softmax_s(logit) * row(s)[0:d_v],   lse[t,h] = ln sum_s exp(logit_s)
+ * This is what a query that sees at most K positions needs (a prompt's first K tokens, drafted
+ * tokens at short contexts); unlike dsa_sparse_mla_prefill with idx NULL it takes ragged chunks,
+ * any context, and packs the heads of several tokens of a request into one tensor-core tile.
+ * q: device [num_tokens, H, d_v + d_rope] of q_dtype; latent: dim == d_v + d_rope, dtype == q_dtype
+ * (f32 or bf16) or DSA_LATENT_E4M3 (d_v 512, d_rope 64; q bf16 or f32); out: device [num_tokens,
+ * H, d_v] of q_dtype; lse: device f32 [num_tokens, H] or NULL.
+ * workspace: at least dsa_chunk_mla_workspace_size(...) bytes, 256-byte aligned (NULL when 0);
+ * calls that may overlap on the GPU need one each.
+ * A row of the cache that holds infinities or NaN reaches only the tokens that see it.  A block id
+ * outside the pool sets DSA_DEVERR_BLOCK_ID, a quantised row with a bad scale DSA_DEVERR_SCALE; the
+ * row is skipped.  A token all of whose rows are skipped gets out = 0, lse = -inf.
+ * Tensor cores: H <= 128, d_v == 512, d_rope == 64, bf16 q.
+ */
+dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v, int32_t d_rope,
+                         const dsa_paged_cache* latent, const dsa_chunks* chunks,
+                         float softmax_scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, dsa_stream stream);
+
+/* Bytes of workspace dsa_chunk_mla needs for these sizes (0 when none).  Host only. */
+size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
+                                    int32_t max_context);
 
 /* Diagnostic of the bounded waits (no counterpart on the pages): enqueues one kernel whose single
  * thread waits on an mbarrier phase that never completes, with the same bounded wait the

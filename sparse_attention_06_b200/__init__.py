@@ -20,7 +20,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_FAULT = range(5)
-DSA_F32, DSA_BF16, DSA_E4M3 = 0, 1, 2
+DSA_F32, DSA_BF16, DSA_E4M3, DSA_LATENT_E4M3 = 0, 1, 2, 3
+
+LATENT_E4M3_DIM, LATENT_E4M3_BYTES = 576, 640  # elements and data bytes of a quantised latent row
 
 DEVERR_BLOCK_ID = 1
 DEVERR_INDEX = 2
@@ -28,6 +30,8 @@ DEVERR_REQUEST = 4
 DEVERR_NAN_SCORE = 8
 DEVERR_TIMEOUT = 16
 DEVERR_QUERY_GROUP = 32
+DEVERR_SCALE = 64
+DEVERR_NONFINITE = 128
 
 # Symbols the C ABI exports (checked by the CPU test suite).
 EXPORTED = (
@@ -35,7 +39,8 @@ EXPORTED = (
     "dsa_sparse_mla_prefill", "dsa_mla_workspace_size", "dsa_get_device_error",
     "dsa_clear_device_error", "dsa_status_string", "dsa_last_error_message", "dsa_abi_version",
     "dsa_kernel_launch_count", "dsa_sparse_mla_decode_noalloc", "dsa_selftest_bounded_wait",
-    "dsa_indexer_topk_workspace_size", "dsa_selftest_gather_rate",
+    "dsa_indexer_topk_workspace_size", "dsa_selftest_gather_rate", "dsa_cache_append", "dsa_cache_read",
+    "dsa_chunk_mla", "dsa_chunk_mla_workspace_size",
 )
 
 
@@ -63,6 +68,13 @@ class _Batch(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class _Chunks(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_reqs", ctypes.c_int32),
+                ("cu_tokens", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32),
+                ("max_context", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -76,7 +88,7 @@ def load_library():
             "libdsa.so not found at %s; build it with `python -m sparse_attention_06_b200.build`" % LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    PC, PB = ctypes.POINTER(_PagedCache), ctypes.POINTER(_Batch)
+    PC, PB, PK = ctypes.POINTER(_PagedCache), ctypes.POINTER(_Batch), ctypes.POINTER(_Chunks)
     sig = {
         "dsa_indexer_scores": [P, I32, P, I32, I32, P, PC, PB, P, I64, P, P],
         "dsa_topk_select": [P, I64, P, I32, I32, P, P, P],
@@ -84,6 +96,9 @@ def load_library():
         "dsa_sparse_mla_decode": [P, I32, I32, I32, I32, PC, PB, P, I32, F, P, P, P, ctypes.c_size_t, P],
         "dsa_sparse_mla_prefill": [P, I32, I32, I32, I32, PC, PB, P, I32, F, P, P, P, ctypes.c_size_t, P],
         "dsa_sparse_mla_decode_noalloc": [P, I32, I32, I32, I32, PC, PB, P, I32, F, P, P, P],
+        "dsa_cache_append": [P, I64, P, I64, I32, PC, PC, PK, P],
+        "dsa_cache_read": [PC, PK, P, I32, P],
+        "dsa_chunk_mla": [P, I32, I32, I32, I32, PC, PK, F, P, P, P, ctypes.c_size_t, P],
         "dsa_get_device_error": [ctypes.POINTER(I32), P],
         "dsa_clear_device_error": [P],
         "dsa_selftest_bounded_wait": [I64, P],
@@ -97,6 +112,8 @@ def load_library():
     lib.dsa_mla_workspace_size.restype = ctypes.c_size_t
     lib.dsa_indexer_topk_workspace_size.argtypes = [I32]
     lib.dsa_indexer_topk_workspace_size.restype = ctypes.c_size_t
+    lib.dsa_chunk_mla_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    lib.dsa_chunk_mla_workspace_size.restype = ctypes.c_size_t
     lib.dsa_status_string.argtypes = [ctypes.c_int]
     lib.dsa_status_string.restype = ctypes.c_char_p
     lib.dsa_last_error_message.restype = ctypes.c_char_p
@@ -142,12 +159,29 @@ def _dtype_code(t: torch.Tensor) -> int:
 @dataclasses.dataclass
 class PagedCache:
     """A paged per-token cache: data [num_blocks, block_size, dim] (f32 / bf16 / e4m3 codes as
-    uint8), scale [num_blocks, block_size] f32 for e4m3."""
+    uint8), scale [num_blocks, block_size] f32 for e4m3.  A quantised latent cache has data
+    [num_blocks, 64, 640] uint8 (512 e4m3 codes, 64 RoPE elements in bf16) and scale
+    [num_blocks, 64, 4] f32, powers of two (include/dsa.h)."""
     data: torch.Tensor
     scale: Optional[torch.Tensor] = None
 
+    @property
+    def dim(self) -> int:
+        """Elements of a row."""
+        return LATENT_E4M3_DIM if self._quantised_latent() else self.data.shape[2]
+
+    def _quantised_latent(self) -> bool:
+        return self.scale is not None and self.scale.dim() == 3
+
     def _c(self) -> _PagedCache:
         nb, bs, dim = self.data.shape
+        if self._quantised_latent():
+            if _dtype_code(self.data) != DSA_E4M3 or dim != LATENT_E4M3_BYTES:
+                raise ValueError("a quantised latent cache has data [num_blocks, 64, 640] uint8")
+            if self.scale.dtype != torch.float32 or tuple(self.scale.shape) != (nb, bs, 4):
+                raise ValueError("a quantised latent cache has scale [num_blocks, 64, 4] float32")
+            return _PagedCache(_dev_ptr(self.data, "cache data"), _dev_ptr(self.scale, "cache scale"), nb, bs,
+                               LATENT_E4M3_DIM, DSA_LATENT_E4M3, 0)
         return _PagedCache(_dev_ptr(self.data, "cache data"), _dev_ptr(self.scale, "cache scale"),
                            nb, bs, dim, _dtype_code(self.data), 0)
 
@@ -170,6 +204,34 @@ class Batch:
         return _Batch(self.q_req.numel(), B, _dev_ptr(self.q_req, "q_req"), _dev_ptr(self.q_pos, "q_pos"),
                       _dev_ptr(self.block_table, "block_table"), mb, int(self.max_context),
                       int(self.query_group), 0)
+
+
+@dataclasses.dataclass
+class Chunks:
+    """Chunks of new tokens of several requests, side by side: cu_tokens [B + 1], seq_len [B] and
+    block_table [B, max_blocks] int32 CUDA tensors; max_context bounds seq_len (host int)."""
+    cu_tokens: torch.Tensor
+    seq_len: torch.Tensor
+    block_table: torch.Tensor
+    max_context: int
+
+    def _c(self, num_tokens) -> _Chunks:
+        for n in ("cu_tokens", "seq_len", "block_table"):
+            if getattr(self, n).dtype != torch.int32:
+                raise ValueError("%s must be int32" % n)
+        B, mb = self.block_table.shape
+        if self.cu_tokens.shape != (B + 1,) or self.seq_len.shape != (B,):
+            raise ValueError("cu_tokens must have B + 1 entries and seq_len B, for the B rows of block_table")
+        return _Chunks(int(num_tokens), B, _dev_ptr(self.cu_tokens, "cu_tokens"), _dev_ptr(self.seq_len, "seq_len"),
+                       _dev_ptr(self.block_table, "block_table"), mb, int(self.max_context))
+
+
+def _same_device(*tensors):
+    """The library runs on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
 
 
 def dsa_indexer_scores(q, w, keys: PagedCache, batch: Batch, scores, stream=None, q_scale=None, key_hist=None):
@@ -254,6 +316,82 @@ def dsa_sparse_mla_decode_noalloc(q, latent: PagedCache, batch: Batch, idx, soft
                                              idx.shape[1], float(softmax_scale), _dev_ptr(out, "out"),
                                              _dev_ptr(lse, "lse"), _stream(stream)))
     return out
+
+
+def _rows(x, dim, what):
+    """Pointer and row stride (elements) of [num_tokens, dim] inputs whose rows may be apart."""
+    if x.dim() != 2 or x.shape[1] != dim:
+        raise ValueError("%s must be [num_tokens, %d]" % (what, dim))
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < dim):
+        raise ValueError("%s: the elements of a row must be contiguous, and rows must not overlap" % what)
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else dim
+
+
+def dsa_cache_append(k, kv, keys: Optional[PagedCache], latent: Optional[PagedCache], chunks: Chunks, stream=None):
+    """Writes the new tokens' indexer keys k [num_tokens, key dim] and latent rows kv
+    [num_tokens, 576] into their paged caches, quantising where a cache is quantised
+    (include/dsa.h).  k and keys, or kv and latent, may be None; rows of k and kv may be apart
+    (a slice of a wider projection)."""
+    lib = load_library()
+    if (k is None) != (keys is None) or (kv is None) != (latent is None):
+        raise ValueError("k comes with keys, and kv with latent")
+    given = [x for x in (k, kv) if x is not None]
+    if not given:
+        raise ValueError("nothing to append")
+    if len(given) == 2 and (k.shape[0] != kv.shape[0] or k.dtype != kv.dtype):
+        raise ValueError("k and kv must have the same tokens and dtype")
+    kc = keys._c() if keys is not None else None
+    lc = latent._c() if latent is not None else None
+    cc = chunks._c(given[0].shape[0])
+    _same_device(k, kv, chunks.cu_tokens, *(c.data for c in (keys, latent) if c is not None))
+    kp, ks = _rows(k, kc.dim, "k") if kc is not None else (None, 0)
+    vp, vs = _rows(kv, lc.dim, "kv") if lc is not None else (None, 0)
+    if given[0].shape[0] == 0:
+        return
+    _check(lib.dsa_cache_append(kp, ks, vp, vs, _dtype_code(given[0]), ctypes.byref(kc) if kc is not None else None,
+                                ctypes.byref(lc) if lc is not None else None, ctypes.byref(cc), _stream(stream)))
+
+
+def dsa_cache_read(cache: PagedCache, chunks: Chunks, out, stream=None):
+    """out[t] = the values of the cached row at token t's position; out [num_tokens, row elements]
+    bf16 or f32 (include/dsa.h)."""
+    lib = load_library()
+    c = cache._c()
+    if out.dim() != 2 or out.shape[1] != c.dim:
+        raise ValueError("out must be [num_tokens, %d]" % c.dim)
+    cc = chunks._c(out.shape[0])
+    _same_device(cache.data, out, chunks.cu_tokens)
+    if out.shape[0]:
+        _check(lib.dsa_cache_read(ctypes.byref(c), ctypes.byref(cc), _dev_ptr(out, "out"), _dtype_code(out),
+                                  _stream(stream)))
+    return out
+
+
+def dsa_chunk_mla(q, latent: PagedCache, chunks: Chunks, softmax_scale, out, lse=None, workspace=None, stream=None):
+    """Dense MQA-mode MLA of chunks of new tokens: the token at position p attends to the positions
+    0..p of its request (include/dsa.h).  q [num_tokens, H, 576], out [num_tokens, H, 512],
+    workspace of dsa_chunk_mla_workspace_size(...) bytes."""
+    lib = load_library()
+    T, H, dqk = q.shape
+    d_v = out.shape[-1]
+    if tuple(out.shape) != (T, H, d_v) or out.dtype != q.dtype:
+        raise ValueError("out must be [num_tokens, H, d_v] of q's dtype")
+    if lse is not None and (tuple(lse.shape) != (T, H) or lse.dtype != torch.float32):
+        raise ValueError("lse must be [num_tokens, H] float32")
+    lc, cc = latent._c(), chunks._c(T)
+    _same_device(q, latent.data, out, lse, workspace, chunks.cu_tokens)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if T:
+        _check(lib.dsa_chunk_mla(_dev_ptr(q, "q"), _dtype_code(q), H, d_v, dqk - d_v, ctypes.byref(lc),
+                                 ctypes.byref(cc), float(softmax_scale), _dev_ptr(out, "out"), _dev_ptr(lse, "lse"),
+                                 _dev_ptr(workspace, "workspace"), ws_bytes, _stream(stream)))
+    return out
+
+
+def dsa_chunk_mla_workspace_size(num_tokens, num_reqs, H, d_v, max_context) -> int:
+    return int(load_library().dsa_chunk_mla_workspace_size(num_tokens, num_reqs, H, d_v, max_context))
 
 
 def dsa_mla_workspace_size(num_queries, H, d_v, k) -> int:

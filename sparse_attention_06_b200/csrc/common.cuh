@@ -42,6 +42,42 @@ __device__ __forceinline__ float load_elem(const void* base, int dtype, int64_t 
   return e4m3_to_float(static_cast<const uint8_t*>(base)[i]);
 }
 
+// A quantised latent row's group scale: a power of two 2^e, -100 <= e <= 119.
+__device__ __forceinline__ bool latent_scale_ok(float s) {
+  const uint32_t b = __float_as_uint(s);
+  return (b & 0x807FFFFFu) == 0u && (b >> 23) >= 27u && (b >> 23) <= 246u;
+}
+
+// Value of element i of pool row `row`, any cache dtype.
+__device__ __forceinline__ float load_cached(const dsa_paged_cache& c, int64_t row, int i) {
+  if (c.dtype == DSA_LATENT_E4M3) {
+    const uint8_t* p = static_cast<const uint8_t*>(c.data) + row * 640;
+    return i < 512 ? e4m3_to_float(p[i]) * c.scale[row * 4 + (i >> 7)]
+                   : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p + 512)[i - 512]);
+  }
+  const float v = load_elem(c.data, c.dtype, row * c.dim + i);
+  return c.dtype == DSA_E4M3 ? v * c.scale[row] : v;
+}
+
+// Request and position of row t of a call's chunks; false for a row behind the last request, and
+// for one whose request has bounds outside the call's (flagged).
+__device__ __forceinline__ bool chunk_token(const dsa_chunks& c, int t, int* req, int* pos, int* err) {
+  if (t >= c.num_tokens || t < c.cu_tokens[0] || t >= c.cu_tokens[c.num_reqs]) return false;
+  int lo = 0, hi = c.num_reqs;  // cu_tokens[lo] <= t < cu_tokens[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.cu_tokens[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int first = c.cu_tokens[lo], end = c.cu_tokens[lo + 1], len = c.seq_len[lo];
+  if (first < 0 || end > c.num_tokens || len > c.max_context || len < end - first) {
+    raise_error(err, DSA_DEVERR_REQUEST);
+    return false;
+  }
+  *req = lo;
+  *pos = len - (end - t);
+  return true;
+}
+
 // ---------------------------------------------------------------------------------------------
 // order keys of scores (selection) and their digit histogram
 // ---------------------------------------------------------------------------------------------

@@ -105,12 +105,53 @@ dsa_status check_cache(const dsa_paged_cache* c, const dsa_batch* b, const char*
   if (!c->data) return fail(DSA_ERR_INVALID_ARG, "%s cache data is NULL", name);
   if (c->num_blocks < 1 || c->block_size < 1 || c->dim < 1)
     return fail(DSA_ERR_INVALID_ARG, "%s cache has an empty shape", name);
-  if (c->dtype != DSA_F32 && c->dtype != DSA_BF16 && c->dtype != DSA_E4M3)
+  if (c->dtype != DSA_F32 && c->dtype != DSA_BF16 && c->dtype != DSA_E4M3 && c->dtype != DSA_LATENT_E4M3)
     return fail(DSA_ERR_INVALID_ARG, "%s cache dtype is unknown", name);
   if (c->dtype == DSA_E4M3 && !c->scale)
     return fail(DSA_ERR_INVALID_ARG, "%s cache is e4m3 but has no scale", name);
   if (!aligned16(c->data)) return fail(DSA_ERR_INVALID_ARG, "%s cache data is not 16-byte aligned", name);
   if ((int64_t)b->max_blocks * c->block_size < (int64_t)b->max_context)
+    return fail(DSA_ERR_INVALID_ARG, "%s: max_blocks * block_size < max_context", name);
+  return DSA_OK;
+}
+
+// A quantised latent cache's own layout (dtype DSA_LATENT_E4M3; data and sizes as check_cache).
+dsa_status check_latent_e4m3(const dsa_paged_cache* c, const char* name) {
+  if (c->block_size != 64 || c->dim != 576)
+    return fail(DSA_ERR_INVALID_ARG, "%s cache: quantised latent rows need block_size 64 and dim 576", name);
+  if (!c->scale || !aligned16(c->scale))
+    return fail(DSA_ERR_INVALID_ARG, "%s cache: quantised latent rows need a 16-byte aligned scale array", name);
+  return DSA_OK;
+}
+
+dsa_status check_chunks(const dsa_chunks* c) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "chunks is NULL%s");
+  if (c->num_tokens < 0 || c->num_reqs < 0) return fail(DSA_ERR_INVALID_ARG, "chunks: negative size%s");
+  if (c->num_tokens == 0 || c->num_reqs == 0) return DSA_OK;
+  if (!c->cu_tokens || !c->seq_len || !c->block_table)
+    return fail(DSA_ERR_INVALID_ARG, "chunks has a NULL device array%s");
+  if (c->max_blocks < 1 || c->max_context < 1)
+    return fail(DSA_ERR_INVALID_ARG, "chunks needs max_blocks, max_context >= 1%s");
+  return DSA_OK;
+}
+
+// A cache that the chunk calls write, read back or attend to: key_cache tells which quantised dtype it may have.
+dsa_status check_chunk_cache(const dsa_paged_cache* c, const dsa_chunks* ch, const char* name, bool e4m3_keys,
+                             bool e4m3_latent) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "%s cache is NULL", name);
+  if (!c->data || !aligned16(c->data))
+    return fail(DSA_ERR_INVALID_ARG, "%s cache data is NULL or not 16-byte aligned", name);
+  if (c->num_blocks < 1 || c->block_size != 64 || c->dim < 1)
+    return fail(DSA_ERR_INVALID_ARG, "%s cache needs num_blocks >= 1, block_size 64 and dim >= 1", name);
+  if (c->dtype == DSA_LATENT_E4M3 && e4m3_latent) {
+    dsa_status st = check_latent_e4m3(c, name);
+    if (st != DSA_OK) return st;
+  } else if (c->dtype == DSA_E4M3 && e4m3_keys) {
+    if (!c->scale) return fail(DSA_ERR_INVALID_ARG, "%s cache is e4m3 but has no scale", name);
+  } else if (c->dtype != DSA_F32 && c->dtype != DSA_BF16) {
+    return fail(DSA_ERR_INVALID_ARG, "%s cache has a dtype this call does not take", name);
+  }
+  if ((int64_t)ch->max_blocks * 64 < (int64_t)ch->max_context)
     return fail(DSA_ERR_INVALID_ARG, "%s: max_blocks * block_size < max_context", name);
   return DSA_OK;
 }
@@ -151,7 +192,7 @@ MlaPlan mla_plan(bool decode, const void* q, int32_t q_dtype, int32_t H, int32_t
                  const dsa_paged_cache& latent, int32_t T, int32_t k, const void* out, int num_sms) {
   MlaPlan pl{false, 1, 0};
   pl.tensor_cores = (H == 128 || H == 64) && d_v == 512 && d_rope == 64 && q_dtype == DSA_BF16 &&
-                    latent.block_size == 64 && aligned16(q) && aligned16(out) && aligned16(latent.data);
+                    latent.dtype == DSA_BF16 && latent.block_size == 64 && aligned16(q) && aligned16(out) && aligned16(latent.data);
   if (pl.tensor_cores && T > 0) {
     pl.nsplit = decode ? mla_tc_num_splits(T, k, num_sms) : 1;
     pl.workspace_bytes = mla_tc_workspace_bytes(T, H, d_v, pl.nsplit);
@@ -238,6 +279,7 @@ static dsa_status indexer_scores_impl(const void* q, int32_t q_dtype, const floa
   if (!q || !w || !scores) return fail(DSA_ERR_INVALID_ARG, "indexer: NULL q, w or scores%s");
   if (Hi < 1 || Di < 1 || Hi * Di > 16384) return fail(DSA_ERR_INVALID_ARG, "indexer: Hi*Di must be in [1, 16384]%s");
   if (keys->dim != Di) return fail(DSA_ERR_INVALID_ARG, "indexer: key dim != Di%s");
+  if (keys->dtype == DSA_LATENT_E4M3) return fail(DSA_ERR_INVALID_ARG, "indexer: keys must be f32, bf16 or e4m3%s");
   if (q_dtype != DSA_F32 && q_dtype != DSA_BF16 && q_dtype != DSA_E4M3)
     return fail(DSA_ERR_INVALID_ARG, "indexer: q dtype must be f32, bf16 or e4m3%s");
   if (q_dtype == DSA_E4M3 && !q_scale) return fail(DSA_ERR_INVALID_ARG, "indexer: e4m3 q needs q_scale%s");
@@ -333,7 +375,12 @@ static dsa_status mla_common(bool decode, const void* q, int32_t q_dtype, int32_
   if (d_v > 1024 || d_v + d_rope > 4096) return fail(DSA_ERR_INVALID_ARG, "mla: d_v <= 1024 and d_v + d_rope <= 4096 required%s");
   if (latent->dim != d_v + d_rope) return fail(DSA_ERR_INVALID_ARG, "mla: latent dim != d_v + d_rope%s");
   if (q_dtype != DSA_F32 && q_dtype != DSA_BF16) return fail(DSA_ERR_INVALID_ARG, "mla: dtype must be f32 or bf16%s");
-  if (latent->dtype != q_dtype) return fail(DSA_ERR_INVALID_ARG, "mla: latent dtype != q dtype%s");
+  if (latent->dtype == DSA_LATENT_E4M3) {
+    if (d_v != 512 || d_rope != 64) return fail(DSA_ERR_INVALID_ARG, "mla: a quantised latent cache needs d_v 512 and d_rope 64%s");
+    if ((st = check_latent_e4m3(latent, "latent")) != DSA_OK) return st;
+  } else if (latent->dtype != q_dtype) {
+    return fail(DSA_ERR_INVALID_ARG, "mla: latent dtype != q dtype%s");
+  }
   if (k < 1 || k > 65536) return fail(DSA_ERR_INVALID_ARG, "mla: k must be in [1, 65536]%s");
   if (!(softmax_scale > 0.0f)) return fail(DSA_ERR_INVALID_ARG, "mla: softmax_scale must be > 0%s");
   int* err;
@@ -374,6 +421,81 @@ dsa_status dsa_sparse_mla_prefill(const void* q, int32_t q_dtype, int32_t H, int
                                   size_t workspace_bytes, dsa_stream stream) {
   return mla_common(false, q, q_dtype, H, d_v, d_rope, latent, batch, idx, k, softmax_scale, out,
                     lse, workspace, workspace_bytes, stream);
+}
+
+dsa_status dsa_cache_append(const void* k, int64_t k_stride, const void* kv, int64_t kv_stride,
+                            int32_t x_dtype, const dsa_paged_cache* keys,
+                            const dsa_paged_cache* latent, const dsa_chunks* chunks,
+                            dsa_stream stream) {
+  dsa_status st = check_chunks(chunks);
+  if (st != DSA_OK) return st;
+  if ((k == nullptr) != (keys == nullptr) || (kv == nullptr) != (latent == nullptr))
+    return fail(DSA_ERR_INVALID_ARG, "append: k comes with keys and kv with latent%s");
+  if (chunks->num_tokens == 0 || chunks->num_reqs == 0 || (!k && !kv)) return DSA_OK;
+  if (x_dtype != DSA_F32 && x_dtype != DSA_BF16) return fail(DSA_ERR_INVALID_ARG, "append: inputs must be f32 or bf16%s");
+  if (keys && (st = check_chunk_cache(keys, chunks, "indexer key", true, false)) != DSA_OK) return st;
+  if (latent && (st = check_chunk_cache(latent, chunks, "latent", false, true)) != DSA_OK) return st;
+  if ((k && k_stride < keys->dim) || (kv && kv_stride < latent->dim))
+    return fail(DSA_ERR_INVALID_ARG, "append: an input row is shorter than the cache's%s");
+  AppendArgs a = {};
+  int sms;
+  if (!device_state(&a.err, &sms)) return fail(DSA_ERR_CUDA, "no CUDA device%s");
+  a.k = k;
+  a.k_stride = k_stride;
+  a.kv = kv;
+  a.kv_stride = kv_stride;
+  a.x_dtype = x_dtype;
+  if (keys) a.keys = *keys;
+  if (latent) a.latent = *latent;
+  a.chunks = *chunks;
+  return cuda_status(launch_cache_append(a, static_cast<cudaStream_t>(stream)), "dsa_cache_append launch", 1);
+}
+
+dsa_status dsa_cache_read(const dsa_paged_cache* cache, const dsa_chunks* chunks, void* out,
+                          int32_t out_dtype, dsa_stream stream) {
+  dsa_status st = check_chunks(chunks);
+  if (st != DSA_OK) return st;
+  if (chunks->num_tokens == 0 || chunks->num_reqs == 0) return DSA_OK;
+  if ((st = check_chunk_cache(cache, chunks, "read", true, true)) != DSA_OK) return st;
+  if (!out) return fail(DSA_ERR_INVALID_ARG, "read: out is NULL%s");
+  if (out_dtype != DSA_F32 && out_dtype != DSA_BF16) return fail(DSA_ERR_INVALID_ARG, "read: out must be f32 or bf16%s");
+  ReadArgs a{*cache, *chunks, out, out_dtype, nullptr};
+  int sms;
+  if (!device_state(&a.err, &sms)) return fail(DSA_ERR_CUDA, "no CUDA device%s");
+  return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)), "dsa_cache_read launch", 1);
+}
+
+dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v, int32_t d_rope,
+                         const dsa_paged_cache* latent, const dsa_chunks* chunks,
+                         float softmax_scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, dsa_stream stream) {
+  dsa_status st = check_chunks(chunks);
+  if (st != DSA_OK) return st;
+  if (chunks->num_tokens == 0 || chunks->num_reqs == 0) return DSA_OK;
+  if ((st = check_chunk_cache(latent, chunks, "latent", false, true)) != DSA_OK) return st;
+  if (!q || !out) return fail(DSA_ERR_INVALID_ARG, "chunk mla: NULL q or out%s");
+  if (H < 1 || d_v < 1 || d_rope < 0) return fail(DSA_ERR_INVALID_ARG, "chunk mla: bad H, d_v or d_rope%s");
+  if (d_v > 1024 || d_v + d_rope > 4096)
+    return fail(DSA_ERR_INVALID_ARG, "chunk mla: d_v <= 1024 and d_v + d_rope <= 4096 required%s");
+  if (latent->dim != d_v + d_rope) return fail(DSA_ERR_INVALID_ARG, "chunk mla: latent dim != d_v + d_rope%s");
+  if (q_dtype != DSA_F32 && q_dtype != DSA_BF16) return fail(DSA_ERR_INVALID_ARG, "chunk mla: q must be f32 or bf16%s");
+  if (latent->dtype == DSA_LATENT_E4M3) {
+    if (d_v != 512) return fail(DSA_ERR_INVALID_ARG, "chunk mla: a quantised latent cache needs d_v 512 and d_rope 64%s");
+  } else if (latent->dtype != q_dtype) {
+    return fail(DSA_ERR_INVALID_ARG, "chunk mla: latent dtype != q dtype%s");
+  }
+  if (!(softmax_scale > 0.0f)) return fail(DSA_ERR_INVALID_ARG, "chunk mla: softmax_scale must be > 0%s");
+  int* err;
+  int sms;
+  if (!device_state(&err, &sms)) return fail(DSA_ERR_CUDA, "no CUDA device%s");
+  MlaArgs a{q, q_dtype, H, d_v, d_rope, *latent, {}, nullptr, chunks->max_context, softmax_scale, out, lse,
+            workspace, workspace_bytes, err};
+  return cuda_status(launch_chunk_mla_generic(a, *chunks, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch", 1);
+}
+
+size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
+                                    int32_t max_context) {
+  return 0;
 }
 
 dsa_status dsa_selftest_bounded_wait(int64_t limit_cycles, dsa_stream stream) {

@@ -19,14 +19,14 @@ namespace {
 
 constexpr int kGenericTile = 128;
 
-__device__ __forceinline__ bool lookup_row(const dsa_batch& b, const dsa_paged_cache& c, int req,
-                                           int64_t pos, int64_t* row, int* err) {
+__device__ __forceinline__ bool lookup_row(const int32_t* block_table, int max_blocks, const dsa_paged_cache& c,
+                                           int req, int64_t pos, int64_t* row, int* err) {
   int64_t lblk = pos / c.block_size;
-  if (lblk >= b.max_blocks) {
+  if (lblk >= max_blocks) {
     raise_error(err, DSA_DEVERR_BLOCK_ID);
     return false;
   }
-  int32_t blk = b.block_table[(int64_t)req * b.max_blocks + lblk];
+  int32_t blk = block_table[(int64_t)req * max_blocks + lblk];
   if (blk < 0 || blk >= c.num_blocks) {
     raise_error(err, DSA_DEVERR_BLOCK_ID);
     return false;
@@ -58,7 +58,7 @@ __global__ void indexer_generic_kernel(IndexerArgs a) {
   const int64_t s = s0 + threadIdx.x;
   if (s > pos) return;
   int64_t row;
-  if (!lookup_row(a.batch, a.keys, req, s, &row, a.err)) return;
+  if (!lookup_row(a.batch.block_table, a.batch.max_blocks, a.keys, req, s, &row, a.err)) return;
   const float sc = (a.keys.dtype == DSA_E4M3) ? a.keys.scale[row] : 1.0f;
   const int64_t kbase = row * a.Di;
   float score = 0.0f;
@@ -90,20 +90,16 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return tot;
 }
 
-// grid (H, T), block 128: one CTA per (query, head), rows visited in order with a running max.
-__global__ void mla_generic_kernel(MlaArgs a) {
+// One CTA's (query t, head h), rows visited in order with a running max; the query sits at
+// position pos of request req.  With keep_nan a NaN among the visible rows makes out and lse NaN;
+// without it such a query gets out = 0 and lse = -inf, as one that sees no row does.
+__device__ void mla_generic_row(const MlaArgs& a, const int32_t* block_table, int max_blocks, int t, int h, int req,
+                                int pos, bool keep_nan) {
   extern __shared__ float sm[];
   const int dqk = a.d_v + a.d_rope;
   float* qs = sm;          // [dqk]
   float* red = sm + dqk;   // [32]
-  const int h = blockIdx.x, t = blockIdx.y;
-  const int req = a.batch.q_req[t];
-  const int pos = a.batch.q_pos[t];
   const int64_t qo = ((int64_t)t * a.H + h);
-  if (req < 0 || req >= a.batch.num_reqs || pos < 0 || pos >= a.batch.max_context) {
-    if (threadIdx.x == 0 && h == 0) raise_error(a.err, DSA_DEVERR_REQUEST);
-    return;
-  }
   for (int i = threadIdx.x; i < dqk; i += blockDim.x) qs[i] = load_elem(a.q, a.dtype, qo * dqk + i);
   __syncthreads();
   float m = -INFINITY, l = 0.0f;
@@ -120,11 +116,18 @@ __global__ void mla_generic_kernel(MlaArgs a) {
       continue;
     }
     int64_t row;
-    if (!lookup_row(a.batch, a.latent, req, p, &row, threadIdx.x == 0 ? a.err : nullptr)) continue;
-    const int64_t rb = row * dqk;
+    if (!lookup_row(block_table, max_blocks, a.latent, req, p, &row, threadIdx.x == 0 ? a.err : nullptr)) continue;
+    if (a.latent.dtype == DSA_LATENT_E4M3) {
+      bool ok = true;
+      for (int g = 0; g < 4; ++g) ok = ok && latent_scale_ok(a.latent.scale[row * 4 + g]);
+      if (!ok) {
+        if (threadIdx.x == 0) raise_error(a.err, DSA_DEVERR_SCALE);
+        continue;
+      }
+    }
     float part = 0.0f;
     for (int i = threadIdx.x; i < dqk; i += blockDim.x)
-      part = fmaf(qs[i], load_elem(a.latent.data, a.latent.dtype, rb + i), part);
+      part = fmaf(qs[i], load_cached(a.latent, row, i), part);
     const float logit = block_sum(part, red) * a.scale;
     const float m_new = fmaxf(m, logit);
     const float corr = expf(m - m_new);
@@ -133,11 +136,12 @@ __global__ void mla_generic_kernel(MlaArgs a) {
 #pragma unroll
     for (int c = 0; c < kMaxVPerThread; ++c) {
       const int col = threadIdx.x + c * blockDim.x;
-      if (col < a.d_v) o[c] = fmaf(pe, load_elem(a.latent.data, a.latent.dtype, rb + col), o[c] * corr);
+      if (col < a.d_v) o[c] = fmaf(pe, load_cached(a.latent, row, col), o[c] * corr);
     }
     m = m_new;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const bool some = keep_nan ? l != 0.0f : l > 0.0f;
+  const float inv = some ? 1.0f / l : 0.0f;
 #pragma unroll
   for (int c = 0; c < kMaxVPerThread; ++c) {
     const int col = threadIdx.x + c * blockDim.x;
@@ -148,7 +152,27 @@ __global__ void mla_generic_kernel(MlaArgs a) {
     else
       static_cast<__nv_bfloat16*>(a.out)[qo * a.d_v + col] = __float2bfloat16_rn(v);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[qo] = l > 0.0f ? m + logf(l) : -INFINITY;
+  if (a.lse && threadIdx.x == 0) a.lse[qo] = some ? m + logf(l) : -INFINITY;
+}
+
+// grid (H, T), block 128: one CTA per (query, head).
+__global__ void mla_generic_kernel(MlaArgs a) {
+  const int h = blockIdx.x, t = blockIdx.y;
+  const int req = a.batch.q_req[t];
+  const int pos = a.batch.q_pos[t];
+  if (req < 0 || req >= a.batch.num_reqs || pos < 0 || pos >= a.batch.max_context) {
+    if (threadIdx.x == 0 && h == 0) raise_error(a.err, DSA_DEVERR_REQUEST);
+    return;
+  }
+  mla_generic_row(a, a.batch.block_table, a.batch.max_blocks, t, h, req, pos, a.latent.dtype == DSA_LATENT_E4M3);
+}
+
+// The dense attention of chunks, same split of work; grid.x = H * num_tokens (CTA x is token x / H).
+__global__ void chunk_mla_generic_kernel(MlaArgs a, dsa_chunks c) {
+  const int t = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  int req, pos;
+  if (!chunk_token(c, t, &req, &pos, threadIdx.x == 0 ? a.err : nullptr)) return;
+  mla_generic_row(a, c.block_table, c.max_blocks, t, h, req, pos, true);
 }
 
 }  // namespace
@@ -173,6 +197,14 @@ cudaError_t launch_mla_generic(const MlaArgs& a, cudaStream_t s) {
   dim3 grid(a.H, T);
   size_t smem = sizeof(float) * ((size_t)a.d_v + a.d_rope + 32);
   mla_generic_kernel<<<grid, kMlaThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_mla_generic(const MlaArgs& a, const dsa_chunks& c, cudaStream_t s) {
+  const int64_t ctas = (int64_t)c.num_tokens * a.H;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  size_t smem = sizeof(float) * ((size_t)a.d_v + a.d_rope + 32);
+  chunk_mla_generic_kernel<<<(unsigned)ctas, kMlaThreads, smem, s>>>(a, c);
   return cudaGetLastError();
 }
 

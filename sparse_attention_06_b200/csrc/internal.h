@@ -41,9 +41,32 @@ struct MlaArgs {
   int* err;
 };
 
+// cache writing and reading
+struct AppendArgs {
+  const void* k;
+  int64_t k_stride;
+  const void* kv;
+  int64_t kv_stride;
+  int x_dtype;
+  dsa_paged_cache keys, latent;
+  dsa_chunks chunks;
+  int* err;
+};
+struct ReadArgs {
+  dsa_paged_cache cache;
+  dsa_chunks chunks;
+  void* out;
+  int out_dtype;
+  int* err;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s);
+
 // generic CUDA-core path (any shape)
 cudaError_t launch_indexer_generic(const IndexerArgs& a, cudaStream_t s);
 cudaError_t launch_mla_generic(const MlaArgs& a, cudaStream_t s);
+// dense attention of chunks: a.batch and a.idx are unused
+cudaError_t launch_chunk_mla_generic(const MlaArgs& a, const dsa_chunks& c, cudaStream_t s);
 
 // radix top-k (any k <= 4096); key_hist (or null): [T, kKeyBins] digit counts of each row's
 // scores, read to place the threshold and left zeroed
