@@ -156,6 +156,11 @@ dsa_status check_chunk_cache(const dsa_paged_cache* c, const dsa_chunks* ch, con
   return DSA_OK;
 }
 
+// Shapes of the chunk attention that run on the tensor cores.
+bool chunk_tensor_cores(int32_t q_dtype, int32_t H, int32_t d_v, int32_t d_rope) {
+  return q_dtype == DSA_BF16 && H >= 1 && H <= 1024 && d_v == 512 && d_rope == 64;
+}
+
 // ---------------------------------------------------------------------------------------------
 // tensor maps
 // ---------------------------------------------------------------------------------------------
@@ -191,9 +196,13 @@ bool current_device_sms(int* num_sms) {
 MlaPlan mla_plan(bool decode, const void* q, int32_t q_dtype, int32_t H, int32_t d_v, int32_t d_rope,
                  const dsa_paged_cache& latent, int32_t T, int32_t k, const void* out, int num_sms) {
   MlaPlan pl{false, 1, 0};
-  pl.tensor_cores = (H == 128 || H == 64) && d_v == 512 && d_rope == 64 && q_dtype == DSA_BF16 &&
-                    latent.dtype == DSA_BF16 && latent.block_size == 64 && aligned16(q) && aligned16(out) && aligned16(latent.data);
-  if (pl.tensor_cores && T > 0) {
+  const bool heads_ok = H == 128 || H == 64;
+  pl.tensor_cores = (heads_ok || (latent.dtype == DSA_LATENT_E4M3 && H >= 1 && H < 128)) && d_v == 512 &&
+                    d_rope == 64 && q_dtype == DSA_BF16 &&
+                    (latent.dtype == DSA_BF16 || latent.dtype == DSA_LATENT_E4M3) && latent.block_size == 64 &&
+                    aligned16(q) && aligned16(out) && aligned16(latent.data);
+  // (other head counts than 64 and 128 have no workspace to split into: its size does not depend on the cache)
+  if (pl.tensor_cores && heads_ok && T > 0) {
     pl.nsplit = decode ? mla_tc_num_splits(T, k, num_sms) : 1;
     pl.workspace_bytes = mla_tc_workspace_bytes(T, H, d_v, pl.nsplit);
   }
@@ -397,7 +406,8 @@ static dsa_status mla_common(bool decode, const void* q, int32_t q_dtype, int32_
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
       return fail(DSA_ERR_INVALID_ARG, "mla: workspace missing, too small or not 256-byte aligned%s");
     kernels = pl.nsplit > 1 ? 2 : 1;
-    e = launch_mla_tc(a, pl.nsplit, sms, static_cast<cudaStream_t>(stream));
+    e = latent->dtype == DSA_LATENT_E4M3 ? launch_mla_quantised_tc(a, pl.nsplit, sms, static_cast<cudaStream_t>(stream))
+                                         : launch_mla_tc(a, pl.nsplit, sms, static_cast<cudaStream_t>(stream));
   } else {
     e = launch_mla_generic(a, static_cast<cudaStream_t>(stream));
   }
@@ -490,12 +500,23 @@ dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v,
   if (!device_state(&err, &sms)) return fail(DSA_ERR_CUDA, "no CUDA device%s");
   MlaArgs a{q, q_dtype, H, d_v, d_rope, *latent, {}, nullptr, chunks->max_context, softmax_scale, out, lse,
             workspace, workspace_bytes, err};
-  return cuda_status(launch_chunk_mla_generic(a, *chunks, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch", 1);
+  // queries or outputs off a 16-byte boundary cannot be copied as tiles
+  if (!chunk_tensor_cores(q_dtype, H, d_v, d_rope) || !aligned16(q) || !aligned16(out))
+    return cuda_status(launch_chunk_mla_generic(a, *chunks, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch", 1);
+  const int nsplit = chunk_mla_splits(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, sms);
+  const size_t need = chunk_mla_workspace(chunks->num_tokens, chunks->num_reqs, H, nsplit);
+  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return fail(DSA_ERR_INVALID_ARG, "chunk mla: workspace missing, too small or not 256-byte aligned%s");
+  return cuda_status(launch_chunk_mla_tc(a, *chunks, nsplit, sms, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch",
+                     nsplit > 1 ? 2 : 1);
 }
 
 size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
                                     int32_t max_context) {
-  return 0;
+  if (num_tokens < 1 || num_reqs < 1 || max_context < 1 || !chunk_tensor_cores(DSA_BF16, H, d_v, 64)) return 0;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return chunk_mla_workspace(num_tokens, num_reqs, H, chunk_mla_splits(num_tokens, num_reqs, H, max_context, sms));
 }
 
 dsa_status dsa_selftest_bounded_wait(int64_t limit_cycles, dsa_stream stream) {

@@ -1,0 +1,1043 @@
+// mla_packed.cu -- MLA (MQA mode) for tiles of 128 query rows on tcgen05 tensor cores: dense attention of
+// chunks over the paged latent cache, and sparse attention over quantised latents.
+//
+// Mathematics: out = softmax(tau Q K^T + mask) V with K the 576-wide latent rows and V their first
+// 512 elements, by one pass over the keys with a running maximum and sum per query row.
+//
+// Query rows.  A token's H heads are H rows of the [num_tokens * H, 576] query matrix and a chunk's
+// tokens follow each other, so 128 consecutive rows of that matrix are one tensor-core tile whatever H
+// is: with 16 heads a tile holds eight tokens of the request, which share every key tile.  Row r of a
+// tile belongs to token (first row + r) / H of the chunk; the causal mask is the only thing that
+// differs between the tokens of a tile.  (Sparse attention: one query per tile, its keys are its own.)
+//
+// Work unit = (row tile, key split sp, value half v), as in the bf16 sparse kernel: O of 128 rows x
+// 512 values in f32 would fill tensor memory, so two CTAs take 256 values each and both compute S.
+// Per 64-key tile: S = Q K^T (M = 128, N = 64, K = 576), softmax, O_v += P V_v (N = 256, K = 64).
+// Tensor memory: O_v [0, 256), S [256, 320), Q dims 0..383 [320, 512); Q dims 384..575 (48 KB), P
+// (16 KB) and a two-stage ring of bf16 key tiles (2 x 72 KB, 128B-swizzled: K-major B of Q K^T and
+// MN-major B of P V at once) are in shared memory.
+//
+// Quantised latents become bf16 on their way into the ring: eight warps load a row's 512 codes with
+// 16-byte loads (one tile ahead, into registers), turn them into bf16 (exact: a code has four
+// significant bits and its scale is a power of two) and store them in the swizzled layout.  bf16
+// latents come by TMA: whole 64-token pages as nine 64-row boxes, a page's visible part by gather4.
+//
+// Roles (14 warps): 0-7 fill the ring and move Q into tensor memory (staged by TMA through the ring's
+// idle stages at the start of a unit); 8 issues Q K^T, 9 issues P V (each the whole warp, so that the
+// compiler keeps the issue uniform: with elect.sync one M = 128, N = 64 product is issued every ~32
+// cycles, against ~60 from a thread chosen by its index); 10-13 softmax and epilogue, one row per thread.
+// All waits are bounded; bad rows set the device error word and are skipped.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kDqk = 576, kDv = 512, kHalf = 256;
+constexpr int kRows = 128;               // query rows per tile (MMA M)
+constexpr int kTile = 64;                // keys per tile = tokens per page
+constexpr int kChunks = 9;               // 64-dim column blocks of a row
+constexpr int kTmemQChunks = 6;          // of these in tensor memory for Q
+constexpr int kStages = 2;
+constexpr int kFillWarps = 8;
+constexpr int kKeysPerWarp = kTile / kFillWarps;  // 8
+constexpr int kQkWarp = 8, kPvWarp = 9, kSoftmaxWarp = 10;
+constexpr int kThreads = 32 * 14;
+constexpr int kLatentBytes = 640;        // data bytes of a quantised row
+
+constexpr int K_CHUNK = kTile * 128;
+constexpr int K_BYTES = kChunks * K_CHUNK;
+constexpr int Q_CHUNK = kRows * 128;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + (kChunks - kTmemQChunks) * Q_CHUNK;
+constexpr int OFF_P = OFF_K + kStages * K_BYTES;
+constexpr int OFF_BAR = OFF_P + kRows * kTile * 2;
+constexpr int NBAR = 20;
+constexpr int OFF_MASK = OFF_BAR + NBAR * 8;           // [stage] 64-bit mask of real rows (a byte per warp)
+constexpr int OFF_POISON = OFF_MASK + kStages * 8;     // [stage] rows with NaN or infinity, see below
+constexpr int OFF_MISC = OFF_POISON + kStages * 8;
+constexpr int OFF_STATS = OFF_MISC + 32;               // 1 / l of each row (last unit)
+constexpr int SMEM = OFF_STATS + kRows * 4 + 1024;
+static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(3 * Q_CHUNK <= K_BYTES, "three Q boxes are staged in a ring stage");
+
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320, TM_COLS = 512;
+
+// Where a unit's keys come from.
+enum Source {
+  kSelected,   // quantised rows chosen per query by idx (or every visible position)
+  kPages,      // quantised rows at consecutive positions
+  kPagesBf16,  // bf16 rows at consecutive positions
+};
+
+struct Params {
+  const uint8_t* data;    // pool rows
+  const float* scale;     // quantised: [pool rows, 4]
+  const int32_t* idx;     // kSelected: [T, k] or null (every visible position)
+  const int32_t *q_req, *q_pos;
+  dsa_chunks chunks;      // kPages*
+  const int32_t* block_table;
+  __nv_bfloat16* out;     // [T, H, 512]
+  float* lse;             // [T, H] or null
+  float *part_o, *part_lse;  // several splits: [tiles, nsplit, prows, 512] and [tiles, nsplit, prows]
+  int32_t num_blocks, oob_row;
+  int T, H, k, ks, nsplit, prows, tiles, num_reqs, max_blocks, max_context;
+  float scale_log2;       // softmax scale * log2(e)
+  int* err;
+};
+
+// A unit of work (rows 0 of an unused one: nothing to do).
+struct Unit {
+  int rows;       // query rows in use
+  int row0;       // first of them in the [T * H] query rows
+  int req;        // request (-1: the query is invalid, it sees nothing)
+  int tok0, h0;   // kPages*: token of row 0 within its chunk's positions (its position), its head
+  int lo, hi;     // keys: selection slots or positions [lo, hi)
+  int prow;       // first partial row
+  int v;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error ~2^-22; 2^-inf = 0
+  return y;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Tiles of a batch of chunks: request r has the tile numbers first_tile(r) .. first_tile(r + 1) - 1, at
+// least as many as its rows need (ceil(b - a) <= floor(b) - floor(a) + 1); the rest are unused.  So a
+// tile's request follows from cu_tokens alone, by a search instead of a prefix sum.
+__host__ __device__ __forceinline__ int64_t first_tile(int64_t cu, int r, int H) { return cu * H / kRows + r; }
+
+// Request of tile `tile` (warp-collective): a 32-way search of the last r with first_tile(r) <= tile;
+// -1 when there is none.
+__device__ __forceinline__ int tile_request(const dsa_chunks& c, int H, int tile) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = c.num_reqs;  // candidates lo .. lo + n - 1
+  while (true) {
+    const int step = (n + 31) / 32;
+    const int r = lo + lane * step;
+    const bool le = lane * step < n && first_tile(max(0, c.cu_tokens[r]), r, H) <= tile;
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, le);
+    if (b == 0u) return -1;
+    const int last = 31 - __clz(b);
+    lo += last * step;
+    n = min(step, n - last * step);
+    if (step == 1) return lo;
+  }
+}
+
+// Keys of split sp of a row tile that sees positions 0 .. len - 1: whole key tiles, evenly.
+__device__ __forceinline__ void split_range(int len, int nsplit, int sp, int& lo, int& hi) {
+  const int tiles = (len + kTile - 1) / kTile;
+  const int per = (tiles + nsplit - 1) / nsplit;
+  lo = min(len, sp * per * kTile);
+  hi = min(len, lo + per * kTile);
+}
+
+// Row tile `i` of request r: its rows, the position of its first and behind its last token.
+__device__ __forceinline__ bool chunk_tile(const dsa_chunks& c, int H, int r, int i, int& rows, int& row0, int& tok0, int& h0,
+                                           int& len, int* err) {
+  const int first = c.cu_tokens[r], end = c.cu_tokens[r + 1], seq = c.seq_len[r];
+  if (first == end) return false;
+  if (first < 0 || end < first || end > c.num_tokens || seq > c.max_context || seq < end - first) {
+    raise_error(err, DSA_DEVERR_REQUEST);
+    return false;
+  }
+  const int64_t all = (int64_t)(end - first) * H, f = (int64_t)i * kRows;
+  if (f >= all) return false;
+  rows = (int)min((int64_t)kRows, all - f);
+  row0 = (int)((int64_t)first * H + f);
+  const int ctx = seq - (end - first);
+  tok0 = ctx + (int)(f / H);
+  h0 = (int)(f % H);
+  len = ctx + (int)((f + rows - 1) / H) + 1;
+  return true;
+}
+
+// Unit u, by a whole warp.  Chunks: late tiles first (they see the most keys of a prompt).
+template <Source kSrc>
+__device__ __forceinline__ Unit get_unit(const Params& p, int u, int* err) {
+  Unit x;
+  x.rows = 0;
+  x.v = u & 1;
+  const int ts = u >> 1;
+  const int sp = ts % p.nsplit;
+  int tile = ts / p.nsplit;
+  if constexpr (kSrc == kSelected) {
+    x.rows = p.H;
+    x.row0 = tile * p.H;
+    x.req = p.q_req[tile];
+    x.tok0 = p.q_pos[tile];
+    x.h0 = 0;
+    if (x.req < 0 || x.req >= p.num_reqs || x.tok0 < 0 || x.tok0 >= p.max_context) {
+      raise_error(err, DSA_DEVERR_REQUEST);
+      x.req = -1;
+    }
+    const int slots = p.idx ? p.k : (x.req < 0 ? 0 : min(p.k, x.tok0 + 1));
+    x.lo = min(slots, sp * p.ks);
+    x.hi = min(slots, x.lo + p.ks);
+  } else {
+    tile = p.tiles - 1 - tile;
+    const int r = tile_request(p.chunks, p.H, tile);
+    if (r < 0) return x;
+    int len;
+    const int i = tile - (int)first_tile(max(0, p.chunks.cu_tokens[r]), r, p.H);
+    if (!chunk_tile(p.chunks, p.H, r, i, x.rows, x.row0, x.tok0, x.h0, len, err)) {
+      x.rows = 0;
+      return x;
+    }
+    x.req = r;
+    split_range(len, p.nsplit, sp, x.lo, x.hi);
+    if (x.lo >= x.hi) x.rows = 0;  // (a split without keys leaves no partial: the combine knows it)
+  }
+  x.prow = (tile * p.nsplit + sp) * p.prows;
+  return x;
+}
+
+// Eight codes (two words) times a power of two, as four bf16 pairs: the code's exponent and mantissa
+// are moved to a bf16's, whose value is then the code's times 2^-120 (subnormal codes become
+// subnormal bf16), and one exact product by 2^(e + 120) does the rest; `m2` (1 unless e > 7, where 2^(e + 120) is
+// no bf16) takes what is left.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t m, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+  lo = mul_bf16x2(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), m);
+  hi = mul_bf16x2(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), m);
+}
+
+// O_v / l of this warp's 32 rows, columns [c_lo, c_hi) (multiples of 64), from tensor memory to the
+// partials (f32) or the output (bf16) through a 4 KB staging area: lane i stages its row's 128-byte block
+// with its 16-byte pieces permuted, then the warp writes whole 128-byte pieces of four rows at a time.
+__device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t lane_base, int quarter, int c_lo, int c_hi,
+                                        uint8_t* stage, float inv, bool have_o) {
+  const int lane = threadIdx.x & 31;
+  const int srow = lane >> 3, spiece = lane & 7;
+  const bool f32out = p.nsplit > 1;
+  const int rows = min(32, x.rows - quarter * 32);
+  auto flush = [&](int col) {
+    __syncwarp();
+#pragma unroll
+    for (int k4 = 0; k4 < 8; ++k4) {
+      const int rr = k4 * 4 + srow;
+      const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((spiece ^ (rr & 7)) << 4));
+      if (rr < rows) {
+        if (f32out)
+          *reinterpret_cast<uint4*>(p.part_o + ((int64_t)x.prow + quarter * 32 + rr) * kDv + x.v * kHalf + col + spiece * 4) = y;
+        else
+          *reinterpret_cast<uint4*>(p.out + ((int64_t)x.row0 + quarter * 32 + rr) * kDv + x.v * kHalf + col + spiece * 8) = y;
+      }
+    }
+    __syncwarp();
+  };
+  if (rows <= 0) return;
+#pragma unroll 1
+  for (int c0 = c_lo; c0 < c_hi; c0 += 64) {
+    uint32_t o[64];
+    if (have_o) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_O + c0 + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) o[c] = 0u;
+    }
+    uint8_t* mine = stage + lane * 128;
+    if (f32out) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = 32 * b + 4 * j;
+          *reinterpret_cast<float4*>(mine + ((j ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv, __uint_as_float(o[c + 2]) * inv,
+                          __uint_as_float(o[c + 3]) * inv);
+        }
+        flush(c0 + 32 * b);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 hv =
+              __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+          pk[e] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        *reinterpret_cast<uint4*>(mine + ((j ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+      flush(c0);
+    }
+  }
+}
+
+template <Source kSrc>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
+                      const __grid_constant__ CUtensorMap pmap, const Params p) {
+  constexpr bool kQuant = kSrc != kPagesBf16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem + OFF_Q;
+  uint8_t* k_ring = smem + OFF_K;
+  uint8_t* p_s = smem + OFF_P;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* k_full = bars + 0;      // [kStages] rows of the tile in place, masks published
+  uint64_t* k_empty = bars + 2;     // [kStages] P V of the stage done
+  uint64_t* land = bars + 4;        // [kStages] bf16 rows landed, to be looked over before k_full
+  uint64_t* q_stage = bars + 6;     // [2] the unit's Q: boxes 0-2; boxes 3-5 and the shared-memory part
+  uint64_t* q_read = bars + 8;      // staged Q read: the ring stages may be filled
+  uint64_t* q_full = bars + 9;      // Q of the unit in place
+  uint64_t* q_empty = bars + 10;    // the unit's last Q K^T has completed
+  uint64_t* s_full = bars + 11;
+  uint64_t* s_empty = bars + 12;
+  uint64_t* p_full = bars + 13;
+  uint64_t* pv_done = bars + 14;
+  uint64_t* fin = bars + 15;        // both issuing warps' products have completed
+  uint64_t* ep_last = bars + 16;    // last unit: 1 / l published after its last P V
+  uint8_t* masks = smem + OFF_MASK;
+  uint8_t* poisons = smem + OFF_POISON;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
+  float* stats = reinterpret_cast<float*>(smem + OFF_STATS);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = p.tiles * p.nsplit * 2;
+  griddep_launch_dependents();
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&k_full[i], kFillWarps);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&land[i], kFillWarps);
+      mbar_init(&q_stage[i], 1);
+    }
+    mbar_init(q_read, kFillWarps);
+    mbar_init(q_full, 32 * kFillWarps);
+    mbar_init(q_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 4);
+    mbar_init(p_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(fin, 2);
+    mbar_init(ep_last, 128);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kQkWarp) {
+    tmem_alloc(tmem_slot, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+
+  // the CTA's last unit that has work (its epilogue is shared among the warps)
+  int last_u = -1;
+  if (warp < kFillWarps || warp >= kSoftmaxWarp) {
+    for (int u = blockIdx.x + (units - 1 - (int)blockIdx.x) / (int)gridDim.x * (int)gridDim.x; u >= 0; u -= gridDim.x)
+      if (get_unit<kSrc>(p, u, nullptr).rows) {
+        last_u = u;
+        break;
+      }
+  }
+
+  if (warp < kFillWarps) {
+    // ------------------------------------------------------------------ ring and Q
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int half = lane >> 4, l16 = lane & 15;  // quantised rows: two at a time, 16 lanes each
+    int gi = 0, ui = 0;
+    uint32_t nland[kStages] = {0u, 0u};
+    bool ok = true;
+    int staged = 0;  // warp 0 lane 0: Q copies issued for the unit in hand
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit x = get_unit<kSrc>(p, u, tid == 0 && (u & 1) == 0 ? p.err : nullptr);
+      if (!x.rows) continue;
+      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+      const bool report = x.v == 0;
+
+      // --- row lookup: kSelected: lane j < 8 has key 8 warp + j of a tile, selected position two tiles
+      // ahead and page one tile ahead; kPages*: every lane has the tile's page
+      const int kbase = warp * kKeysPerWarp + lane;
+      auto slot_pos = [&](int j) -> int {
+        const int slot = x.lo + j * kTile + kbase;
+        if (lane >= kKeysPerWarp || j >= ntiles || slot >= x.hi) return -1;
+        if (!p.idx) return slot;
+        const int ps = p.idx[(int64_t)(x.row0 / p.H) * p.k + slot];
+        if (ps < -1 || ps > x.tok0) {
+          if (report && x.req >= 0) raise_error(p.err, DSA_DEVERR_INDEX);
+          return -1;
+        }
+        return x.req < 0 ? -1 : ps;
+      };
+      auto page_of = [&](int lblk) -> int {
+        const int blk = lblk < p.max_blocks ? p.block_table[(int64_t)x.req * p.max_blocks + lblk] : -1;
+        if (blk < 0 || blk >= p.num_blocks) {
+          if (report) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+          return -1;
+        }
+        return blk;
+      };
+      // pool row of this lane's key of tile j (kSelected; from its position and page), or of the lane's
+      // row 8 warp + lane % 8 of the page (kPages*); -1 when there is none to see
+      auto pool_row = [&](int j, int ps, int blk) -> int {
+        if constexpr (kSrc == kSelected) return blk >= 0 ? blk * kTile + ps % kTile : -1;
+        const int r = warp * kKeysPerWarp + (lane & 7);
+        return blk >= 0 && x.lo + j * kTile + r < x.hi ? blk * kTile + r : -1;
+      };
+      int ps0 = -1, ps1 = -1, blk0 = -1, blk1 = -1;  // of the tile whose rows are looked up next, and the one after
+      if constexpr (kSrc == kSelected) {
+        ps0 = slot_pos(0);
+        ps1 = slot_pos(1);
+        blk0 = ps0 >= 0 ? page_of(ps0 / kTile) : -1;
+      } else {
+        blk0 = page_of(x.lo / kTile);
+        blk1 = ntiles > 1 ? page_of(x.lo / kTile + 1) : -1;
+      }
+      // pool row of tile j, advancing the pipeline (called for j = 0, 1, 2, ...)
+      auto next_row = [&](int j) -> int {
+        const int row = j < ntiles ? pool_row(j, ps0, blk0) : -1;
+        if constexpr (kSrc == kSelected) {
+          blk0 = ps1 >= 0 ? page_of(ps1 / kTile) : -1;
+          ps0 = ps1;
+          ps1 = slot_pos(j + 2);
+        } else {
+          blk0 = blk1;
+          blk1 = j + 2 < ntiles ? page_of(x.lo / kTile + j + 2) : -1;
+        }
+        return row;
+      };
+
+      // --- quantised rows in flight: pair q is the rows 8 warp + 2 q + half; word group hh its dims
+      // 256 hh + 16 l16 .. + 15
+      uint4 code[4][2], rope[2];
+      float sc[4][2];
+      auto load_pair = [&](int rw, int q) {
+        const int row = __shfl_sync(0xFFFFFFFFu, rw, 2 * q + half);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          code[q][hh] = make_uint4(0u, 0u, 0u, 0u);
+          sc[q][hh] = 1.0f;
+          if (row >= 0) {
+            code[q][hh] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + 256 * hh) + l16);
+            sc[q][hh] = __ldg(p.scale + (int64_t)row * 4 + 2 * hh + (l16 >> 3));
+          }
+        }
+      };
+      auto load_rope = [&](int rw, int i) {
+        const int row = __shfl_sync(0xFFFFFFFFu, rw, 4 * i + (lane >> 3));
+        rope[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= 0) rope[i] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + kDv) + (lane & 7));
+      };
+      int row_n = next_row(0);  // rows of the tile in registers (quantised) or about to be copied
+      if constexpr (kQuant) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_pair(row_n, q);
+        load_rope(row_n, 0);
+        load_rope(row_n, 1);
+      }
+
+      // --- Q of the unit: boxes 0-5 through the ring's stages into tensor memory, 6-8 to their place
+      const int s0 = gi % kStages, s1 = (gi + 1) % kStages;
+      if (ui >= 1 && !(ok = warp_wait(q_empty, (ui - 1) & 1, p.err, abort_flag))) break;
+      if (gi >= 2 && !(ok = warp_wait(&k_empty[s0], ((gi / kStages) - 1) & 1, p.err, abort_flag))) break;
+      if (tid == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&q_stage[0], 3 * Q_CHUNK);
+        for (int c = 0; c < 3; ++c) tma_load_2d(k_ring + s0 * K_BYTES + c * Q_CHUNK, &qmap, &q_stage[0], c * 64, x.row0);
+        staged = 1;
+      }
+      // (gi counts whole tiles, so stage s1 was last used by tile gi - 1)
+      if (gi >= 1 && !(ok = warp_wait(&k_empty[s1], ((gi - 1) / kStages) & 1, p.err, abort_flag))) break;
+      if (tid == 0) {
+        mbar_arrive_expect_tx(&q_stage[1], 6 * Q_CHUNK);
+        for (int c = 3; c < 6; ++c) tma_load_2d(k_ring + s1 * K_BYTES + (c - 3) * Q_CHUNK, &qmap, &q_stage[1], c * 64, x.row0);
+        for (int c = 6; c < kChunks; ++c) tma_load_2d(q_s + (c - 6) * Q_CHUNK, &qmap, &q_stage[1], c * 64, x.row0);
+        staged = 2;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        if (!(ok = warp_wait(&q_stage[b], ui & 1, p.err, abort_flag))) break;
+        const int r = quarter * 32 + lane;
+        const uint8_t* src = k_ring + (b ? s1 : s0) * K_BYTES + r * 128;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {  // this warp's half (64 bytes) of the row's block
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + c * Q_CHUNK + (((part * 4 + e) ^ (r & 7)) << 4));
+            w[4 * e] = y.x; w[4 * e + 1] = y.y; w[4 * e + 2] = y.z; w[4 * e + 3] = y.w;
+          }
+          tmem_st16(my_lanes + TM_Q + (3 * b + c) * 32 + part * 16, w);
+        }
+      }
+      if (!ok) break;
+      staged = 0;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_read);
+      if (!(ok = warp_wait(q_read, ui & 1, p.err, abort_flag))) break;
+      ++ui;
+
+      // --- the unit's key tiles
+      for (int j = 0; j < ntiles; ++j, ++gi) {
+        const int s = gi % kStages;
+        const int row = row_n;
+        row_n = next_row(j + 1);
+        if (gi >= kStages && !(ok = warp_wait(&k_empty[s], ((gi / kStages) - 1) & 1, p.err, abort_flag))) break;
+        uint8_t* stage = k_ring + s * K_BYTES;
+        if constexpr (kQuant) {
+          const uint32_t seen = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
+          uint32_t valid = seen, poison = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = warp * kKeysPerWarp + 2 * q + half;
+            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc[q][0]) || !latent_scale_ok(sc[q][1]));
+            const bool drop = half ? (bad >> 16) != 0u : (bad & 0xFFFFu) != 0u;  // the row's scales are no powers of two
+            if (bad) valid &= ~(((bad & 0xFFFFu) ? 1u : 0u) << (2 * q) | ((bad >> 16) ? 2u : 0u) << (2 * q));
+            uint32_t nan = 0u;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t w[4] = {code[q][hh].x, code[q][hh].y, code[q][hh].z, code[q][hh].w};
+              const uint32_t e = __float_as_uint(sc[q][hh]) >> 23;  // biased exponent of the scale
+              // 2^(e - 127 + 120) as a bf16 pair, at most 2^127; what is left above that in m2
+              const uint32_t e1 = min(e + 120u, 254u);
+              const uint32_t m1 = e1 << 7 | e1 << 23;
+              if (drop) w[0] = w[1] = w[2] = w[3] = 0u;
+              uint32_t b[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                nan |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: that code is NaN
+                decode4(w[i], m1, b[2 * i], b[2 * i + 1]);
+              }
+              if (e > 134u) {  // scales above 2^7
+                const uint32_t e2 = min(e, 246u) - 134u + 127u;
+                const uint32_t m2 = e2 << 7 | e2 << 23;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(b[i], m2);
+              }
+              // dims 256 hh + 16 l16 ..: column block 4 hh + l16 / 4, pieces 2 (l16 % 4) and the next; the
+              // two rows of a pair differ in bit 0 of r, so their pieces cover all eight bank groups
+              uint8_t* dst = stage + (4 * hh + (l16 >> 2)) * K_CHUNK + r * 128;
+              const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
+              *reinterpret_cast<uint4*>(dst + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+              *reinterpret_cast<uint4*>(dst + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
+            }
+            const uint32_t np = __ballot_sync(0xFFFFFFFFu, (nan & 0x80808080u) != 0u);
+            poison |= (((np & 0xFFFFu) ? 1u : 0u) | ((np >> 16) ? 2u : 0u)) << (2 * q);
+            load_pair(row_n, q);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r8 = 4 * i + (lane >> 3);
+            const int r = warp * kKeysPerWarp + r8;
+            *reinterpret_cast<uint4*>(stage + 8 * K_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
+                (valid >> r8) & 1u ? rope[i] : make_uint4(0u, 0u, 0u, 0u);
+            load_rope(row_n, i);
+          }
+          if (lane == 0) {
+            masks[s * 8 + warp] = (uint8_t)valid;
+            poisons[s * 8 + warp] = (uint8_t)(poison & valid);
+          }
+          if (report && seen != valid && lane == 0) raise_error(p.err, DSA_DEVERR_SCALE);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[s]);
+        } else {
+          const uint32_t valid = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
+          const int base = x.lo + j * kTile;
+          const int prow0 = __shfl_sync(0xFFFFFFFFu, row, 0) - warp * kKeysPerWarp;  // the page's first row
+          const bool whole = base + kTile <= x.hi && valid == 0xFFu;
+          // rows that only some of the tile's tokens see: a NaN there must not reach the others through
+          // 0 * NaN in P V.  They are looked over once they have landed, see below.
+          const bool partly = base + kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
+          uint64_t* bar = partly ? &land[s] : &k_full[s];
+          if (lane == 0) {
+            masks[s * 8 + warp] = (uint8_t)valid;
+            if (!partly) poisons[s * 8 + warp] = 0;
+            fence_proxy_async_smem();
+            if (whole) {
+              if (warp == 0) {
+                mbar_arrive_expect_tx(bar, K_BYTES);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) tma_load_2d(stage + c * K_CHUNK, &pmap, bar, c * 64, prow0);
+              } else {
+                mbar_arrive(bar);
+              }
+            } else {
+              mbar_arrive_expect_tx(bar, kKeysPerWarp * kDqk * 2);
+            }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int g4 = 0; g4 < 2; ++g4) {
+              const int rc = row >= 0 ? row : p.oob_row;
+              const int r0 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4), r1 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 1);
+              const int r2 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 2), r3 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 3);
+              if (lane == 0) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                  tma_gather4(stage + c * K_CHUNK + (warp * kKeysPerWarp + 4 * g4) * 128, &rmap, bar, c * 64, r0, r1, r2, r3);
+              }
+            }
+          }
+          if (partly) {
+            if (!(ok = warp_wait(&land[s], nland[s] & 1, p.err, abort_flag))) break;
+            ++nland[s];
+            // values that are not finite become zero and their row is noted: the softmax makes the weights
+            // of the tokens that see it NaN, the others' products stay as they are
+            uint32_t poison = 0u;
+            for (int r8 = 0; r8 < kKeysPerWarp; ++r8) {
+              const int r = warp * kKeysPerWarp + r8;
+              if (base + r <= x.tok0 || base + r >= x.hi) continue;
+              bool found = false;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {  // 64 pieces of 16 bytes: the 512 values
+                const int i = lane + 32 * e;
+                uint4* at = reinterpret_cast<uint4*>(stage + (i >> 3) * K_CHUNK + r * 128 + ((i & 7) << 4));
+                uint4 y = *at;
+                uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                bool f = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; f = true; }
+                  if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; f = true; }
+                }
+                if (f) *at = make_uint4(w[0], w[1], w[2], w[3]);
+                found |= f;
+              }
+              if (__any_sync(0xFFFFFFFFu, found)) poison |= 1u << r8;
+            }
+            if (lane == 0) poisons[s * 8 + warp] = (uint8_t)poison;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[s]);
+          }
+        }
+      }
+      if (!ok) break;
+      if (u == last_u) {
+        // the CTA's last unit: columns [64, 128) and [128, 256) of O_v / l, staged in the ring (free after the last P V)
+        if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
+        tc_fence_after();
+        store_o(p, x, my_lanes, quarter, part ? 128 : 64, part ? 256 : 128, k_ring + warp * 4096, stats[quarter * 32 + lane], ntiles > 0);
+        tc_fence_before();
+      }
+    }
+    if (!ok && tid == 0) {
+      // gave up: copies in flight must land before the CTA exits
+      if (staged >= 1) mbar_wait(&q_stage[0], ui & 1, p.err, nullptr);
+      if (staged >= 2) mbar_wait(&q_stage[1], ui & 1, p.err, nullptr);
+    }
+    if (!ok && !kQuant && lane == 0) {
+      for (int t = gi; t >= 0 && t > gi - kStages; --t)
+        if (t < gi) mbar_wait(&k_full[t % kStages], (uint32_t)((t / kStages) & 1), p.err, nullptr);
+      for (int i = 0; i < kStages; ++i)
+        if (nland[i]) mbar_wait(&land[i], (nland[i] - 1) & 1, p.err, nullptr);
+    }
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------------ Q K^T
+    const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
+    const uint64_t qd = sw128_desc(smem_u32(q_s), 16, 1024);
+    const uint32_t d_s = tmem + TM_S, a_q = tmem + TM_Q;
+    int gi = 0, ui = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit x = get_unit<kSrc>(p, u, nullptr);
+      if (!x.rows) continue;
+      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+      if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
+      ++ui;
+      if (ntiles == 0) {
+        if (elect_one()) mma_commit(q_empty);
+        __syncwarp();
+      }
+      for (int j = 0; j < ntiles; ++j, ++gi) {
+        const int s = gi % kStages;
+        if (!(ok = warp_wait(&k_full[s], (gi / kStages) & 1, p.err, abort_flag))) break;
+        if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
+        tc_fence_after();
+        const uint64_t kd = sw128_desc(smem_u32(k_ring + s * K_BYTES), 16, 1024);
+        constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
+        if (elect_one()) {
+          umma_ts<0>(d_s, a_q, kd, idesc_s);
+#pragma unroll
+          for (int i = 1; i < 4 * kTmemQChunks; ++i)
+            umma_ts<1>(d_s, a_q + (uint32_t)(i * 8), kd + (uint64_t)(i >> 2) * kc + (uint64_t)(i & 3) * 2, idesc_s);
+#pragma unroll
+          for (int i = 0; i < 4 * (kChunks - kTmemQChunks); ++i)
+            umma_ss<1>(d_s, qd + (uint64_t)(i >> 2) * qc + (uint64_t)(i & 3) * 2,
+                       kd + (uint64_t)(kTmemQChunks + (i >> 2)) * kc + (uint64_t)(i & 3) * 2, idesc_s);
+          mma_commit(s_full);
+          if (j == ntiles - 1) mma_commit(q_empty);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) mma_commit(fin);
+    __syncwarp();
+    mbar_wait(fin, 0, p.err, nullptr);
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------------ P V
+    const uint32_t idesc_o = idesc_f16(1u, 1u, (uint32_t)kRows, (uint32_t)kHalf);
+    const uint64_t pd = noswz_desc(smem_u32(p_s), 128, 1024);
+    const uint32_t d_o = tmem + TM_O;
+    int gi = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit x = get_unit<kSrc>(p, u, nullptr);
+      if (!x.rows) continue;
+      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+      for (int j = 0; j < ntiles; ++j, ++gi) {
+        const int s = gi % kStages;
+        if (!(ok = warp_wait(p_full, gi & 1, p.err, abort_flag))) break;
+        tc_fence_after();
+        const uint64_t vd = sw128_desc(smem_u32(k_ring + s * K_BYTES) + (uint32_t)(x.v * 4 * K_CHUNK), K_CHUNK, 1024);
+        if (elect_one()) {
+          if (j > 0)
+            umma_ss<1>(d_o, pd, vd, idesc_o);
+          else
+            umma_ss<0>(d_o, pd, vd, idesc_o);
+          umma_ss<1>(d_o, pd + 16, vd + 128, idesc_o);
+          umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
+          umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
+          mma_commit(pv_done);
+          mma_commit(&k_empty[s]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) mma_commit(fin);
+    __syncwarp();
+    mbar_wait(fin, 0, p.err, nullptr);
+  } else {
+    // ------------------------------------------------------------------ softmax and epilogue
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    int gi = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit x = get_unit<kSrc>(p, u, nullptr);
+      if (!x.rows) continue;
+      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+      // last position this row sees (kSelected: the tile's own mask tells)
+      int limit;
+      if constexpr (kSrc == kSelected)
+        limit = r < x.rows ? 0x7FFFFFFF : -1;
+      else
+        limit = r < x.rows ? x.tok0 + (x.h0 + r) / p.H : -1;
+      float m_used = -INFINITY, l = 0.0f;
+      for (int j = 0; j < ntiles; ++j, ++gi) {
+        const int s = gi % kStages;
+        if (!(ok = warp_wait(s_full, gi & 1, p.err, abort_flag))) break;
+        if (!(ok = warp_wait(&k_full[s], (gi / kStages) & 1, p.err, abort_flag))) break;  // (long past: orders the masks)
+        tc_fence_after();
+        uint32_t sv[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_S + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
+        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + s * 8);
+        const uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + s * 8);
+        const int d = limit - (x.lo + j * kTile);  // this row sees the tile's keys 0 .. d
+        if (d < 63) valid &= d < 0 ? 0ull : (2ull << d) - 1ull;
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        float mt = -INFINITY;
+        if (__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float xv = __uint_as_float(sv[c]) * p.scale_log2;
+            sv[c] = __float_as_uint(xv);
+            mt = fmaxf(mt, xv);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float xv = ((poison >> c) & 1u) ? __uint_as_float(0x7FC00000u) : __uint_as_float(sv[c]) * p.scale_log2;
+            xv = ((valid >> c) & 1u) ? xv : -INFINITY;
+            sv[c] = __float_as_uint(xv);
+            mt = fmaxf(mt, xv);
+          }
+        }
+        if (gi >= 1 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+        // Lazy rescale: the base m_used moves only when some row's maximum exceeds it by more than 2^8
+        // (P stays <= 256), for the whole warp since the tensor-memory accesses are warp-collective.
+        if (__any_sync(0xFFFFFFFFu, mt > m_used + 8.0f)) {
+          const float m_new = fmaxf(m_used, mt);
+          const float f = m_new == -INFINITY ? 1.0f : exp2f(m_used - m_new);  // 0 when m_used = -inf
+          if (j > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < kHalf; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+              tmem_ld16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+              tmem_st16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+              tmem_st16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+            }
+            tmem_wait_st();
+          }
+          l *= f;
+          m_used = m_new;
+        }
+        float psum = 0.0f;
+        uint32_t pk[32];
+        const float msub = m_used == -INFINITY ? 0.0f : m_used;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float p0 = fast_exp2(__uint_as_float(sv[c]) - msub);
+          const float p1 = fast_exp2(__uint_as_float(sv[c + 1]) - msub);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          // the normaliser sums the rounded weights that P V uses
+          const float2 bf = __bfloat1622float2(b);
+          psum += bf.x + bf.y;
+          pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        l += psum;
+        uint8_t* prow = p_s + (r >> 3) * 1024 + (r & 7) * 16;
+#pragma unroll
+        for (int kc = 0; kc < 8; ++kc)
+          *reinterpret_cast<uint4*>(prow + kc * 128) = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      if (ntiles > 0 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+      tc_fence_after();
+      // a row that saw nothing: 0 and -inf; NaN stays NaN
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float lse = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+      if (u == last_u) {
+        stats[r] = inv;
+        mbar_arrive(ep_last);
+      }
+      store_o(p, x, lane_base, quarter, 0, u == last_u ? 64 : kHalf, p_s + quarter * 4096, inv, ntiles > 0);
+      if (x.v == 0 && r < x.rows) {
+        if (p.nsplit == 1) {
+          if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;
+        } else {
+          p.part_lse[(int64_t)x.prow + r] = lse;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kQkWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TM_COLS);
+  }
+}
+
+// grid (T, H), block 128: merge the split partials of one query row, out = sum_sp w_sp O_sp with
+// w_sp = exp(LSE_sp - LSE); thread i sums the value columns 4 i .. 4 i + 3.
+constexpr int kMaxSplits = 64;
+template <bool kChunk>
+__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+  __shared__ float wts[kMaxSplits];
+  __shared__ float s_inv, s_lse;
+  const int t = blockIdx.x, h = blockIdx.y;
+  griddep_launch_dependents();
+  griddep_wait();
+  int tile = t, r = h, n = p.nsplit;
+  if constexpr (kChunk) {
+    int req, pos;
+    if (!chunk_token(p.chunks, t, &req, &pos, nullptr)) return;
+    const int64_t flat = (int64_t)(t - p.chunks.cu_tokens[req]) * p.H + h;
+    const int i = (int)(flat / kRows);
+    r = (int)(flat % kRows);
+    tile = (int)first_tile(p.chunks.cu_tokens[req], req, p.H) + i;
+    int rows, row0, tok0, h0, len;
+    if (!chunk_tile(p.chunks, p.H, req, i, rows, row0, tok0, h0, len, nullptr)) return;
+    const int tiles = (len + kTile - 1) / kTile, per = (tiles + n - 1) / n;
+    n = (tiles + per - 1) / per;  // splits that have keys
+  }
+  const int64_t base = (int64_t)tile * p.nsplit * p.prows + r;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    float v[2], mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int sp = lane + 32 * e;
+      v[e] = sp < n ? p.part_lse[base + (int64_t)sp * p.prows] : -INFINITY;
+      mx = fmaxf(mx, v[e]);
+    }
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[e] = v[e] == -INFINITY ? 0.0f : expf(v[e] - mx);
+      wts[lane + 32 * e] = v[e];
+      sum += v[e];
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) {
+      s_inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      s_lse = sum == 0.0f ? -INFINITY : mx + logf(sum);
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4* src = reinterpret_cast<const float4*>(p.part_o + base * kDv) + threadIdx.x;
+  const int64_t step = (int64_t)p.prows * kDv / 4;
+  for (int sp0 = 0; sp0 < n; sp0 += 16) {
+    float4 a[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a[e] = sp0 + e < n ? __ldg(src + (sp0 + e) * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float w = sp0 + e < n ? wts[sp0 + e] : 0.0f;
+      acc.x = fmaf(w, a[e].x, acc.x);
+      acc.y = fmaf(w, a[e].y, acc.y);
+      acc.z = fmaf(w, a[e].z, acc.z);
+      acc.w = fmaf(w, a[e].w, acc.w);
+    }
+  }
+  const float inv = s_inv;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 pk;
+  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+  const int64_t row = (int64_t)t * p.H + h;
+  *reinterpret_cast<uint2*>(p.out + row * kDv + 4 * threadIdx.x) = pk;
+  if (p.lse && threadIdx.x == 0) p.lse[row] = s_lse;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <Source kSrc>
+cudaError_t launch(Params p, const MlaArgs& a, int num_sms, cudaStream_t s) {
+  alignas(64) CUtensorMap qmap = {}, rmap = {}, pmap = {};
+  if (!encode_tmap_2d(&qmap, a.q, 2, kDqk, (uint64_t)p.T * p.H, kDqk * 2, 64, kRows, true)) return cudaErrorInvalidValue;
+  const uint64_t pool_rows = (uint64_t)a.latent.num_blocks * kTile;
+  // row numbers are 32-bit
+  if (pool_rows >= 0x7FFFFFFFull || (int64_t)p.T * p.H + kRows >= 0x7FFFFFFFll ||
+      (int64_t)p.tiles * p.nsplit * p.prows >= 0x7FFFFFFFll || (int64_t)p.tiles * p.nsplit * 2 >= 0x7FFFFFFFll)
+    return cudaErrorInvalidValue;
+  if (kSrc == kPagesBf16 && (!encode_tmap_2d(&rmap, a.latent.data, 2, kDqk, pool_rows, kDqk * 2, 64, 1, true) ||
+                             !encode_tmap_2d(&pmap, a.latent.data, 2, kDqk, pool_rows, kDqk * 2, 64, kTile, true)))
+    return cudaErrorInvalidValue;
+  p.data = static_cast<const uint8_t*>(a.latent.data);
+  p.scale = a.latent.scale;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.num_blocks = a.latent.num_blocks;
+  p.oob_row = (int32_t)pool_rows;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.err = a.err;
+  p.part_o = nullptr;
+  p.part_lse = nullptr;
+  if (p.nsplit > 1) {
+    p.part_o = static_cast<float*>(a.workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                          up256((size_t)p.tiles * p.nsplit * p.prows * kDv * sizeof(float)));
+  }
+  const int units = p.tiles * p.nsplit * 2;
+  auto kernel = mla_packed_kernel<kSrc>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attrs[2];
+  const cudaLaunchConfig_t cfg = launch_config(dim3(units < num_sms ? units : num_sms), dim3(kThreads), SMEM, s, attrs);
+  e = cudaLaunchKernelEx(&cfg, kernel, qmap, rmap, pmap, p);
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  cudaLaunchAttribute cattrs[2];
+  const cudaLaunchConfig_t ccfg = launch_config(dim3(p.T, p.H), dim3(128), 0, s, cattrs);
+  return cudaLaunchKernelEx(&ccfg, combine_kernel<kSrc != kSelected>, p);
+}
+
+// Row tiles of a batch of chunks (an upper bound: the device knows the chunks' sizes).
+int64_t chunk_tiles(int num_tokens, int num_reqs, int H) { return first_tile(num_tokens, num_reqs, H); }
+
+}  // namespace
+
+// Key splits of a batch of chunks: as many as fill the SMs.  Cost model in key-tile times, as for the
+// sparse kernel: a unit costs its key tiles and a fixed ~3; units run in waves of one per SM; more
+// than one split adds the combine pass.  Only max_context and the numbers of tokens and requests are
+// known here; a request's own length is split evenly on the device.
+int chunk_mla_splits(int num_tokens, int num_reqs, int H, int max_context, int num_sms) {
+  // tiles in use if the tokens are spread evenly over the requests
+  const int64_t per_req = ((int64_t)num_tokens * H + (int64_t)num_reqs * kRows - 1) / ((int64_t)num_reqs * kRows);
+  const double tiles = (double)per_req * (num_reqs < num_tokens ? num_reqs : num_tokens);
+  const int kt = (max_context + kTile - 1) / kTile;
+  double best_cost = 1e300;
+  int best = 1;
+  for (int n = 1; n <= kMaxSplits && n <= kt; n *= 2) {
+    const int per = (kt + n - 1) / n;
+    double units = 2.0 * tiles * n, waves = (double)(int64_t)((units + num_sms - 1) / num_sms);
+    double cost = waves * (per + 3.0);
+    if (n > 1) cost += 3.0 + 0.02 * tiles * n;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int nsplit) {
+  if (nsplit <= 1) return 0;
+  const size_t rows = (size_t)chunk_tiles(num_tokens, num_reqs, H) * nsplit * kRows;
+  return up256(rows * kDv * sizeof(float)) + up256(rows * sizeof(float));
+}
+
+cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int nsplit, int num_sms, cudaStream_t s) {
+  Params p = {};
+  p.chunks = c;
+  p.block_table = c.block_table;
+  p.T = c.num_tokens;
+  p.H = a.H;
+  p.nsplit = nsplit;
+  p.prows = kRows;
+  const int64_t tiles = chunk_tiles(c.num_tokens, c.num_reqs, a.H);
+  if (tiles >= 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  p.tiles = (int)tiles;
+  p.num_reqs = c.num_reqs;
+  p.max_blocks = c.max_blocks;
+  p.max_context = c.max_context;
+  return a.latent.dtype == DSA_BF16 ? launch<kPagesBf16>(p, a, num_sms, s) : launch<kPages>(p, a, num_sms, s);
+}
+
+cudaError_t launch_mla_quantised_tc(const MlaArgs& a, int nsplit, int num_sms, cudaStream_t s) {
+  Params p = {};
+  p.idx = a.idx;
+  p.q_req = a.batch.q_req;
+  p.q_pos = a.batch.q_pos;
+  p.block_table = a.batch.block_table;
+  p.T = p.tiles = a.batch.num_queries;
+  p.H = p.prows = a.H;
+  p.k = a.k;
+  p.nsplit = nsplit;
+  p.ks = ((a.k + nsplit - 1) / nsplit + kTile - 1) / kTile * kTile;
+  p.num_reqs = a.batch.num_reqs;
+  p.max_blocks = a.batch.max_blocks;
+  p.max_context = a.batch.max_context;
+  return launch<kSelected>(p, a, num_sms, s);
+}
+
+}  // namespace dsa
