@@ -13,17 +13,23 @@
 // Work unit = (row tile, key split sp, value half v), as in the bf16 sparse kernel: O of 128 rows x
 // 512 values in f32 would fill tensor memory, so two CTAs take 256 values each and both compute S.
 // Per 64-key tile: S = Q K^T (M = 128, N = 64, K = 576), softmax, O_v += P V_v (N = 256, K = 64).
-// Tensor memory: O_v [0, 256), S [256, 320), Q dims 0..383 [320, 512); Q dims 384..575 (48 KB), P
-// (16 KB) and a two-stage ring of bf16 key tiles (2 x 72 KB, 128B-swizzled: K-major B of Q K^T and
-// MN-major B of P V at once) are in shared memory.
+// Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine 64-dim column blocks [320, 512).  Shared
+// memory: the other three (48 KB), P (16 KB), and the key tile as bf16 in 64-row x 64-dim blocks of 8 KB
+// (128B-swizzled: K-major B of Q K^T and, for the value blocks, MN-major B of P V at once).
 //
-// Quantised latents become bf16 on their way into the ring: eight warps load a row's 512 codes with
+// A tile's nine blocks live in three rings, by how long each is needed: the four blocks of this
+// CTA's values until P V is done (three stages), the other blocks only until Q K^T is (three blocks
+// with two stages, two blocks - the first that Q K^T reads - with one).  So the tensor core can run Q K^T of
+// tile g + 1, P V of tile g and the filling of tile g + 2 at once in 160 KB; whole tiles of 72 KB would
+// leave room for two stages, each held from the first load to the end of P V.
+//
+// Quantised latents become bf16 on their way in: eight warps load a row's 512 codes with
 // 16-byte loads (one tile ahead, into registers), turn them into bf16 (exact: a code has four
 // significant bits and its scale is a power of two) and store them in the swizzled layout.  bf16
 // latents come by TMA: whole 64-token pages as nine 64-row boxes, a page's visible part by gather4.
 //
-// Roles (14 warps): 0-7 fill the ring and move Q into tensor memory (staged by TMA through the ring's
-// idle stages at the start of a unit); 8 issues Q K^T, 9 issues P V (each the whole warp, so that the
+// Roles (14 warps): 0-7 fill the rings and move Q into tensor memory (staged by TMA through idle
+// ring blocks at the start of a unit); 8 issues Q K^T, 9 issues P V (each the whole warp, so that the
 // compiler keeps the issue uniform: with elect.sync one M = 128, N = 64 product is issued every ~32
 // cycles, against ~60 from a thread chosen by its index); 10-13 softmax and epilogue, one row per thread.
 // All waits are bounded; bad rows set the device error word and are skipped.
@@ -40,29 +46,40 @@ constexpr int kDqk = 576, kDv = 512, kHalf = 256;
 constexpr int kRows = 128;               // query rows per tile (MMA M)
 constexpr int kTile = 64;                // keys per tile = tokens per page
 constexpr int kChunks = 9;               // 64-dim column blocks of a row
-constexpr int kTmemQChunks = 6;          // of these in tensor memory for Q
-constexpr int kStages = 2;
+constexpr int kSmemQ = 3;                // Q blocks in shared memory (the first that Q K^T uses), the rest in tensor memory
 constexpr int kFillWarps = 8;
 constexpr int kKeysPerWarp = kTile / kFillWarps;  // 8
 constexpr int kQkWarp = 8, kPvWarp = 9, kSoftmaxWarp = 10;
 constexpr int kThreads = 32 * 14;
 constexpr int kLatentBytes = 640;        // data bytes of a quantised row
 
+// A tile's blocks in the order Q K^T uses them: X0 (RoPE), X1, Y0, Y1, Y2 (the values of the other
+// half), V0 .. V3 (this half's values).
+constexpr int kXBlocks = 2, kYBlocks = 3, kVBlocks = 4;
+constexpr int kYStages = 2, kVStages = 3;
+__device__ __forceinline__ int block_of(int pos, int v) {  // column block of a row at place `pos` of that order
+  return pos == 0 ? 8 : pos < 5 ? 4 * (1 - v) + (pos == 1 ? 3 : pos - 2) : 4 * v + pos - 5;
+}
+
 constexpr int K_CHUNK = kTile * 128;
 constexpr int K_BYTES = kChunks * K_CHUNK;
 constexpr int Q_CHUNK = kRows * 128;
 constexpr int OFF_Q = 0;
-constexpr int OFF_K = OFF_Q + (kChunks - kTmemQChunks) * Q_CHUNK;
-constexpr int OFF_P = OFF_K + kStages * K_BYTES;
-constexpr int OFF_BAR = OFF_P + kRows * kTile * 2;
-constexpr int NBAR = 20;
-constexpr int OFF_MASK = OFF_BAR + NBAR * 8;           // [stage] 64-bit mask of real rows (a byte per warp)
-constexpr int OFF_POISON = OFF_MASK + kStages * 8;     // [stage] rows with NaN or infinity, see below
-constexpr int OFF_MISC = OFF_POISON + kStages * 8;
-constexpr int OFF_STATS = OFF_MISC + 32;               // 1 / l of each row (last unit)
+constexpr int OFF_P = OFF_Q + kSmemQ * Q_CHUNK;
+constexpr int OFF_Y = OFF_P + kRows * kTile * 2;
+constexpr int OFF_X = OFF_Y + kYStages * kYBlocks * K_CHUNK;
+constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;
+constexpr int OFF_BAR = OFF_V + kVStages * kVBlocks * K_CHUNK;
+constexpr int NBAR = 24;
+constexpr int kMaskSlots = 4;
+constexpr int OFF_MASK = OFF_BAR + NBAR * 8;             // [slot] 64-bit mask of real rows (a byte per warp)
+constexpr int OFF_POISON = OFF_MASK + kMaskSlots * 8;    // [slot] rows with NaN or infinity, see below
+constexpr int OFF_MISC = OFF_POISON + kMaskSlots * 8;
+constexpr int OFF_STATS = OFF_MISC + 32;                 // 1 / l of each row (last unit)
 constexpr int SMEM = OFF_STATS + kRows * 4 + 1024;
 static_assert(SMEM <= 232448, "shared memory budget");
-static_assert(3 * Q_CHUNK <= K_BYTES, "three Q boxes are staged in a ring stage");
+static_assert(kYStages * kYBlocks * K_CHUNK == 3 * Q_CHUNK && kXBlocks * K_CHUNK == Q_CHUNK && kVBlocks * K_CHUNK == 2 * Q_CHUNK,
+              "six Q blocks are staged in the Y and X rings and one V stage");
 
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320, TM_COLS = 512;
 
@@ -109,6 +126,26 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// two f32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Tiles of a batch of chunks: request r has the tile numbers first_tile(r) .. first_tile(r + 1) - 1, at
@@ -291,22 +328,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem + OFF_Q;
-  uint8_t* k_ring = smem + OFF_K;
   uint8_t* p_s = smem + OFF_P;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* k_full = bars + 0;      // [kStages] rows of the tile in place, masks published
-  uint64_t* k_empty = bars + 2;     // [kStages] P V of the stage done
-  uint64_t* land = bars + 4;        // [kStages] bf16 rows landed, to be looked over before k_full
-  uint64_t* q_stage = bars + 6;     // [2] the unit's Q: boxes 0-2; boxes 3-5 and the shared-memory part
-  uint64_t* q_read = bars + 8;      // staged Q read: the ring stages may be filled
-  uint64_t* q_full = bars + 9;      // Q of the unit in place
-  uint64_t* q_empty = bars + 10;    // the unit's last Q K^T has completed
-  uint64_t* s_full = bars + 11;
-  uint64_t* s_empty = bars + 12;
-  uint64_t* p_full = bars + 13;
-  uint64_t* pv_done = bars + 14;
-  uint64_t* fin = bars + 15;        // both issuing warps' products have completed
-  uint64_t* ep_last = bars + 16;    // last unit: 1 / l published after its last P V
+  uint64_t* k_full = bars + 0;      // [2] rows of the tile in place, masks published
+  uint64_t* land = bars + 2;        // [2] bf16 rows landed, to be looked over before k_full
+  uint64_t* x_empty = bars + 4;     // Q K^T is past the tile's X blocks
+  uint64_t* y_empty = bars + 5;     // [kYStages] ... past its Y blocks
+  uint64_t* v_empty = bars + 7;     // [kVStages] P V done
+  uint64_t* q_stage = bars + 10;    // the unit's Q landed (staged blocks and shared-memory part)
+  uint64_t* q_read = bars + 11;     // staged Q read: the ring blocks may be filled
+  uint64_t* q_full = bars + 12;     // Q of the unit in place
+  uint64_t* q_empty = bars + 13;    // the unit's last Q K^T has completed
+  uint64_t* s_full = bars + 14;
+  uint64_t* s_empty = bars + 15;
+  uint64_t* p_full = bars + 16;
+  uint64_t* pv_done = bars + 17;
+  uint64_t* fin = bars + 18;        // both issuing warps' products have completed
+  uint64_t* ep_last = bars + 19;    // last unit: 1 / l published after its last P V
   uint8_t* masks = smem + OFF_MASK;
   uint8_t* poisons = smem + OFF_POISON;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -318,12 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], kFillWarps);
-      mbar_init(&k_empty[i], 1);
       mbar_init(&land[i], kFillWarps);
-      mbar_init(&q_stage[i], 1);
     }
+    mbar_init(x_empty, 1);
+    for (int i = 0; i < kYStages; ++i) mbar_init(&y_empty[i], 1);
+    for (int i = 0; i < kVStages; ++i) mbar_init(&v_empty[i], 1);
+    mbar_init(q_stage, 1);
     mbar_init(q_read, kFillWarps);
     mbar_init(q_full, 32 * kFillWarps);
     mbar_init(q_empty, 1);
@@ -357,86 +397,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp < kFillWarps) {
-    // ------------------------------------------------------------------ ring and Q
+    // ------------------------------------------------------------------ rings and Q
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const int half = lane >> 4, l16 = lane & 15;  // quantised rows: two at a time, 16 lanes each
     int gi = 0, ui = 0;
-    uint32_t nland[kStages] = {0u, 0u};
-    bool ok = true;
-    int staged = 0;  // warp 0 lane 0: Q copies issued for the unit in hand
+    uint32_t nland[2] = {0u, 0u};
+    bool ok = true, staged = false;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const Unit x = get_unit<kSrc>(p, u, tid == 0 && (u & 1) == 0 ? p.err : nullptr);
       if (!x.rows) continue;
       const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
       const bool report = x.v == 0;
 
-      // --- row lookup: kSelected: lane j < 8 has key 8 warp + j of a tile, selected position two tiles
-      // ahead and page one tile ahead; kPages*: every lane has the tile's page
-      const int kbase = warp * kKeysPerWarp + lane;
-      auto slot_pos = [&](int j) -> int {
-        const int slot = x.lo + j * kTile + kbase;
+      // --- row lookup, pipelined so that no loaded value is looked at in the tile that loads it.
+      // kSelected: lane j < 8 has key 8 warp + j of a tile: selected position two tiles ahead, page
+      // table entry one tile ahead.  kPages*: every lane has the tile's page table entry.
+      auto load_slot = [&](int j) -> int {
+        const int slot = x.lo + j * kTile + warp * kKeysPerWarp + lane;
         if (lane >= kKeysPerWarp || j >= ntiles || slot >= x.hi) return -1;
-        if (!p.idx) return slot;
-        const int ps = p.idx[(int64_t)(x.row0 / p.H) * p.k + slot];
-        if (ps < -1 || ps > x.tok0) {
-          if (report && x.req >= 0) raise_error(p.err, DSA_DEVERR_INDEX);
-          return -1;
-        }
-        return x.req < 0 ? -1 : ps;
+        return p.idx ? p.idx[(int64_t)(x.row0 / p.H) * p.k + slot] : slot;
       };
-      auto page_of = [&](int lblk) -> int {
-        const int blk = lblk < p.max_blocks ? p.block_table[(int64_t)x.req * p.max_blocks + lblk] : -1;
-        if (blk < 0 || blk >= p.num_blocks) {
-          if (report) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
-          return -1;
-        }
-        return blk;
+      auto load_page = [&](int lblk) -> int {
+        return lblk < p.max_blocks ? p.block_table[(int64_t)x.req * p.max_blocks + lblk] : -1;
       };
-      // pool row of this lane's key of tile j (kSelected; from its position and page), or of the lane's
-      // row 8 warp + lane % 8 of the page (kPages*); -1 when there is none to see
-      auto pool_row = [&](int j, int ps, int blk) -> int {
-        if constexpr (kSrc == kSelected) return blk >= 0 ? blk * kTile + ps % kTile : -1;
-        const int r = warp * kKeysPerWarp + (lane & 7);
-        return blk >= 0 && x.lo + j * kTile + r < x.hi ? blk * kTile + r : -1;
-      };
+      auto visible = [&](int ps) { return x.req >= 0 && ps >= 0 && ps <= x.tok0; };
       int ps0 = -1, ps1 = -1, blk0 = -1, blk1 = -1;  // of the tile whose rows are looked up next, and the one after
       if constexpr (kSrc == kSelected) {
-        ps0 = slot_pos(0);
-        ps1 = slot_pos(1);
-        blk0 = ps0 >= 0 ? page_of(ps0 / kTile) : -1;
+        ps0 = load_slot(0);
+        ps1 = load_slot(1);
+        if (visible(ps0)) blk0 = load_page(ps0 / kTile);
       } else {
-        blk0 = page_of(x.lo / kTile);
-        blk1 = ntiles > 1 ? page_of(x.lo / kTile + 1) : -1;
+        blk0 = load_page(x.lo / kTile);
+        if (ntiles > 1) blk1 = load_page(x.lo / kTile + 1);
       }
-      // pool row of tile j, advancing the pipeline (called for j = 0, 1, 2, ...)
+      // pool row of this lane's key of tile j (kSelected: lanes 0 .. 7, else key 8 warp + lane % 8), -1
+      // when there is none to see; called for j = 0, 1, 2, ...
       auto next_row = [&](int j) -> int {
-        const int row = j < ntiles ? pool_row(j, ps0, blk0) : -1;
-        if constexpr (kSrc == kSelected) {
-          blk0 = ps1 >= 0 ? page_of(ps1 / kTile) : -1;
+        int row = -1;
+        if (kSrc == kSelected) {
+          if (visible(ps0)) {
+            if (blk0 >= 0 && blk0 < p.num_blocks)
+              row = blk0 * kTile + ps0 % kTile;
+            else if (report)
+              raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+          } else if (ps0 != -1 && x.req >= 0 && report) {
+            raise_error(p.err, DSA_DEVERR_INDEX);
+          }
           ps0 = ps1;
-          ps1 = slot_pos(j + 2);
-        } else {
+          ps1 = load_slot(j + 2);
+          blk0 = visible(ps0) ? load_page(ps0 / kTile) : -1;
+        } else if (j < ntiles) {
+          const int r = warp * kKeysPerWarp + (lane & 7);
+          if (blk0 >= 0 && blk0 < p.num_blocks) {
+            if (x.lo + j * kTile + r < x.hi) row = blk0 * kTile + r;
+          } else if (report) {
+            raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+          }
           blk0 = blk1;
-          blk1 = j + 2 < ntiles ? page_of(x.lo / kTile + j + 2) : -1;
+          if (j + 2 < ntiles) blk1 = load_page(x.lo / kTile + j + 2);
         }
         return row;
       };
 
-      // --- quantised rows in flight: pair q is the rows 8 warp + 2 q + half; word group hh its dims
-      // 256 hh + 16 l16 .. + 15
+      // --- quantised rows in flight: pair q is the rows 8 warp + 2 q + half; a lane has 16 of its codes in
+      // this CTA's value half (hh = 0) and 16 in the other (hh = 1)
       uint4 code[4][2], rope[2];
       float sc[4][2];
-      auto load_pair = [&](int rw, int q) {
+      auto load_codes = [&](int rw, int q, int hh) {
         const int row = __shfl_sync(0xFFFFFFFFu, rw, 2 * q + half);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          code[q][hh] = make_uint4(0u, 0u, 0u, 0u);
-          sc[q][hh] = 1.0f;
-          if (row >= 0) {
-            code[q][hh] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + 256 * hh) + l16);
-            sc[q][hh] = __ldg(p.scale + (int64_t)row * 4 + 2 * hh + (l16 >> 3));
-          }
+        const int vh = hh ^ x.v;
+        code[q][hh] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= 0) code[q][hh] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + 256 * vh) + l16);
+      };
+      auto load_scales = [&](int rw, int q) {
+        const int row = __shfl_sync(0xFFFFFFFFu, rw, 2 * q + half);
+        sc[q][0] = sc[q][1] = 1.0f;
+        if (row >= 0) {
+          sc[q][0] = __ldg(p.scale + (int64_t)row * 4 + 2 * x.v + (l16 >> 3));
+          sc[q][1] = __ldg(p.scale + (int64_t)row * 4 + 2 * (1 - x.v) + (l16 >> 3));
         }
       };
       auto load_rope = [&](int rw, int i) {
@@ -447,48 +486,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row_n = next_row(0);  // rows of the tile in registers (quantised) or about to be copied
       if constexpr (kQuant) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_pair(row_n, q);
+        for (int q = 0; q < 4; ++q) {
+          load_scales(row_n, q);
+          load_codes(row_n, q, 0);
+          load_codes(row_n, q, 1);
+        }
         load_rope(row_n, 0);
         load_rope(row_n, 1);
       }
 
-      // --- Q of the unit: boxes 0-5 through the ring's stages into tensor memory, 6-8 to their place
-      const int s0 = gi % kStages, s1 = (gi + 1) % kStages;
+      // --- Q of the unit, once the unit before is past its last Q K^T: places 0 .. 2 of the order to
+      // shared memory, 3 .. 8 through the idle Y and X rings and the V stage next in turn to tensor memory
       if (ui >= 1 && !(ok = warp_wait(q_empty, (ui - 1) & 1, p.err, abort_flag))) break;
-      if (gi >= 2 && !(ok = warp_wait(&k_empty[s0], ((gi / kStages) - 1) & 1, p.err, abort_flag))) break;
+      if (gi >= kVStages && !(ok = warp_wait(&v_empty[gi % kVStages], ((gi / kVStages) - 1) & 1, p.err, abort_flag))) break;
+      uint8_t* v_stage0 = smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK;
       if (tid == 0) {
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&q_stage[0], 3 * Q_CHUNK);
-        for (int c = 0; c < 3; ++c) tma_load_2d(k_ring + s0 * K_BYTES + c * Q_CHUNK, &qmap, &q_stage[0], c * 64, x.row0);
-        staged = 1;
-      }
-      // (gi counts whole tiles, so stage s1 was last used by tile gi - 1)
-      if (gi >= 1 && !(ok = warp_wait(&k_empty[s1], ((gi - 1) / kStages) & 1, p.err, abort_flag))) break;
-      if (tid == 0) {
-        mbar_arrive_expect_tx(&q_stage[1], 6 * Q_CHUNK);
-        for (int c = 3; c < 6; ++c) tma_load_2d(k_ring + s1 * K_BYTES + (c - 3) * Q_CHUNK, &qmap, &q_stage[1], c * 64, x.row0);
-        for (int c = 6; c < kChunks; ++c) tma_load_2d(q_s + (c - 6) * Q_CHUNK, &qmap, &q_stage[1], c * 64, x.row0);
-        staged = 2;
+        mbar_arrive_expect_tx(q_stage, kChunks * Q_CHUNK);
+        for (int c = kSmemQ; c < kChunks; ++c) {
+          const int b = c - kSmemQ;
+          tma_load_2d(b < 4 ? smem + OFF_Y + b * Q_CHUNK : v_stage0 + (b - 4) * Q_CHUNK, &qmap, q_stage, block_of(c, x.v) * 64, x.row0);
+        }
+        for (int c = 0; c < kSmemQ; ++c) tma_load_2d(q_s + c * Q_CHUNK, &qmap, q_stage, block_of(c, x.v) * 64, x.row0);
+        staged = true;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        if (!(ok = warp_wait(&q_stage[b], ui & 1, p.err, abort_flag))) break;
+      if (!(ok = warp_wait(q_stage, ui & 1, p.err, abort_flag))) break;
+      staged = false;
+      {
         const int r = quarter * 32 + lane;
-        const uint8_t* src = k_ring + (b ? s1 : s0) * K_BYTES + r * 128;
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {  // this warp's half (64 bytes) of the row's block
+        for (int b = 0; b < 6; ++b) {  // this warp's half (64 bytes) of the row's block
+          const uint8_t* src = (b < 4 ? smem + OFF_Y + b * Q_CHUNK : v_stage0 + (b - 4) * Q_CHUNK) + r * 128;
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint4 y = *reinterpret_cast<const uint4*>(src + c * Q_CHUNK + (((part * 4 + e) ^ (r & 7)) << 4));
+            const uint4 y = *reinterpret_cast<const uint4*>(src + (((part * 4 + e) ^ (r & 7)) << 4));
             w[4 * e] = y.x; w[4 * e + 1] = y.y; w[4 * e + 2] = y.z; w[4 * e + 3] = y.w;
           }
-          tmem_st16(my_lanes + TM_Q + (3 * b + c) * 32 + part * 16, w);
+          tmem_st16(my_lanes + TM_Q + b * 32 + part * 16, w);
         }
       }
-      if (!ok) break;
-      staged = 0;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(q_full);
@@ -499,65 +537,87 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // --- the unit's key tiles
       for (int j = 0; j < ntiles; ++j, ++gi) {
-        const int s = gi % kStages;
+        const int s = gi & 1, slot = gi % kMaskSlots;
+        uint8_t* v_st = smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK;
+        uint8_t* y_st = smem + OFF_Y + gi % kYStages * kYBlocks * K_CHUNK;
+        uint8_t* x_st = smem + OFF_X;
         const int row = row_n;
         row_n = next_row(j + 1);
-        if (gi >= kStages && !(ok = warp_wait(&k_empty[s], ((gi / kStages) - 1) & 1, p.err, abort_flag))) break;
-        uint8_t* stage = k_ring + s * K_BYTES;
+        auto wait_v = [&]() { return gi < kVStages || warp_wait(&v_empty[gi % kVStages], ((gi / kVStages) - 1) & 1, p.err, abort_flag); };
+        auto wait_y = [&]() { return gi < kYStages || warp_wait(&y_empty[gi % kYStages], ((gi / kYStages) - 1) & 1, p.err, abort_flag); };
+        auto wait_x = [&]() { return gi < 1 || warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag); };
         if constexpr (kQuant) {
           const uint32_t seen = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
           uint32_t valid = seen, poison = 0u;
+          uint32_t drop = 0u;  // bit q: this lane's row of pair q has scales that are no powers of two
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc[q][0]) || !latent_scale_ok(sc[q][1]));
+            if (bad) {
+              valid &= ~(((bad & 0xFFFFu ? 1u : 0u) | (bad >> 16 ? 2u : 0u)) << (2 * q));
+              if (half ? bad >> 16 : bad & 0xFFFFu) drop |= 1u << q;
+            }
+          }
+          // 16 codes into the row's blocks: `dst` is the row of the lane's 64-dim block, pieces 2 (l16 % 4) and
+          // the next; the two rows of a pair differ in bit 0, so a store covers all eight bank groups
+          uint32_t nan[4] = {0u, 0u, 0u, 0u};
+          auto put = [&](int q, int hh, uint8_t* dst, int r) {
+            uint32_t w[4] = {code[q][hh].x, code[q][hh].y, code[q][hh].z, code[q][hh].w};
+            const uint32_t e = __float_as_uint(sc[q][hh]) >> 23;  // biased exponent of the scale
+            // 2^(e - 127 + 120) as a bf16 pair, at most 2^127; what is left above that is m2 below
+            const uint32_t e1 = min(e + 120u, 254u);
+            const uint32_t m1 = e1 << 7 | e1 << 23;
+            if (drop) {
+              if ((drop >> q) & 1u) w[0] = w[1] = w[2] = w[3] = 0u;
+            }
+            uint32_t b[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              nan[q] |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: that code is NaN
+              decode4(w[i], m1, b[2 * i], b[2 * i + 1]);
+            }
+            if (e > 134u) {  // scales above 2^7
+              const uint32_t e2 = min(e, 246u) - 134u + 127u;
+              const uint32_t m2 = e2 << 7 | e2 << 23;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(b[i], m2);
+            }
+            const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
+            *reinterpret_cast<uint4*>(dst + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<uint4*>(dst + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
+          };
+          if (!(ok = wait_v())) break;
+          uint8_t* v_dst = v_st + (l16 >> 2) * K_CHUNK;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int r = warp * kKeysPerWarp + 2 * q + half;
-            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc[q][0]) || !latent_scale_ok(sc[q][1]));
-            const bool drop = half ? (bad >> 16) != 0u : (bad & 0xFFFFu) != 0u;  // the row's scales are no powers of two
-            if (bad) valid &= ~(((bad & 0xFFFFu) ? 1u : 0u) << (2 * q) | ((bad >> 16) ? 2u : 0u) << (2 * q));
-            uint32_t nan = 0u;
+            put(q, 0, v_dst + r * 128, r);
+            load_codes(row_n, q, 0);
+          }
+          if (!(ok = wait_y()) || !(ok = wait_x())) break;
+          uint8_t* o_dst = (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK;
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t w[4] = {code[q][hh].x, code[q][hh].y, code[q][hh].z, code[q][hh].w};
-              const uint32_t e = __float_as_uint(sc[q][hh]) >> 23;  // biased exponent of the scale
-              // 2^(e - 127 + 120) as a bf16 pair, at most 2^127; what is left above that in m2
-              const uint32_t e1 = min(e + 120u, 254u);
-              const uint32_t m1 = e1 << 7 | e1 << 23;
-              if (drop) w[0] = w[1] = w[2] = w[3] = 0u;
-              uint32_t b[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                nan |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: that code is NaN
-                decode4(w[i], m1, b[2 * i], b[2 * i + 1]);
-              }
-              if (e > 134u) {  // scales above 2^7
-                const uint32_t e2 = min(e, 246u) - 134u + 127u;
-                const uint32_t m2 = e2 << 7 | e2 << 23;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(b[i], m2);
-              }
-              // dims 256 hh + 16 l16 ..: column block 4 hh + l16 / 4, pieces 2 (l16 % 4) and the next; the
-              // two rows of a pair differ in bit 0 of r, so their pieces cover all eight bank groups
-              uint8_t* dst = stage + (4 * hh + (l16 >> 2)) * K_CHUNK + r * 128;
-              const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
-              *reinterpret_cast<uint4*>(dst + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
-              *reinterpret_cast<uint4*>(dst + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
-            }
-            const uint32_t np = __ballot_sync(0xFFFFFFFFu, (nan & 0x80808080u) != 0u);
+          for (int q = 0; q < 4; ++q) {
+            const int r = warp * kKeysPerWarp + 2 * q + half;
+            put(q, 1, o_dst + r * 128, r);
+            load_codes(row_n, q, 1);
+            load_scales(row_n, q);
+            const uint32_t np = __ballot_sync(0xFFFFFFFFu, (nan[q] & 0x80808080u) != 0u);
             poison |= (((np & 0xFFFFu) ? 1u : 0u) | ((np >> 16) ? 2u : 0u)) << (2 * q);
-            load_pair(row_n, q);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r8 = 4 * i + (lane >> 3);
             const int r = warp * kKeysPerWarp + r8;
-            *reinterpret_cast<uint4*>(stage + 8 * K_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
                 (valid >> r8) & 1u ? rope[i] : make_uint4(0u, 0u, 0u, 0u);
             load_rope(row_n, i);
           }
           if (lane == 0) {
-            masks[s * 8 + warp] = (uint8_t)valid;
-            poisons[s * 8 + warp] = (uint8_t)(poison & valid);
+            masks[slot * 8 + warp] = (uint8_t)valid;
+            poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
+            if (report && seen != valid) raise_error(p.err, DSA_DEVERR_SCALE);
           }
-          if (report && seen != valid && lane == 0) raise_error(p.err, DSA_DEVERR_SCALE);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_full[s]);
@@ -570,63 +630,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 0 * NaN in P V.  They are looked over once they have landed, see below.
           const bool partly = base + kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
           uint64_t* bar = partly ? &land[s] : &k_full[s];
-          if (lane == 0) {
-            masks[s * 8 + warp] = (uint8_t)valid;
-            if (!partly) poisons[s * 8 + warp] = 0;
-            fence_proxy_async_smem();
+          // this warp's eight rows (or, for a whole page, warp 0 all of them): places lo .. hi - 1 of the order
+          auto copy = [&](int lo, int hi, uint8_t* dst) {
             if (whole) {
-              if (warp == 0) {
-                mbar_arrive_expect_tx(bar, K_BYTES);
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) tma_load_2d(stage + c * K_CHUNK, &pmap, bar, c * 64, prow0);
-              } else {
-                mbar_arrive(bar);
-              }
-            } else {
-              mbar_arrive_expect_tx(bar, kKeysPerWarp * kDqk * 2);
+              if (warp == 0 && lane == 0)
+                for (int c = lo; c < hi; ++c) tma_load_2d(dst + (c - lo) * K_CHUNK, &pmap, bar, block_of(c, x.v) * 64, prow0);
+              return;
             }
-          }
-          if (!whole) {
 #pragma unroll
             for (int g4 = 0; g4 < 2; ++g4) {
               const int rc = row >= 0 ? row : p.oob_row;
               const int r0 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4), r1 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 1);
               const int r2 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 2), r3 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 3);
-              if (lane == 0) {
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                  tma_gather4(stage + c * K_CHUNK + (warp * kKeysPerWarp + 4 * g4) * 128, &rmap, bar, c * 64, r0, r1, r2, r3);
-              }
+              if (lane == 0)
+                for (int c = lo; c < hi; ++c)
+                  tma_gather4(dst + (c - lo) * K_CHUNK + (warp * kKeysPerWarp + 4 * g4) * 128, &rmap, bar, block_of(c, x.v) * 64, r0, r1, r2, r3);
             }
+          };
+          if (!(ok = wait_y())) break;
+          if (lane == 0) {
+            masks[slot * 8 + warp] = (uint8_t)valid;
+            if (!partly) poisons[slot * 8 + warp] = 0;
+            fence_proxy_async_smem();
+            if (!whole)
+              mbar_arrive_expect_tx(bar, kKeysPerWarp * kDqk * 2);
+            else if (warp == 0)
+              mbar_arrive_expect_tx(bar, K_BYTES);
+            else
+              mbar_arrive(bar);
           }
+          __syncwarp();
+          copy(2, 5, y_st);
+          if (!(ok = wait_v())) break;
+          copy(5, 9, v_st);
+          if (!(ok = wait_x())) break;
+          copy(0, 2, x_st);
           if (partly) {
             if (!(ok = warp_wait(&land[s], nland[s] & 1, p.err, abort_flag))) break;
             ++nland[s];
             // values that are not finite become zero and their row is noted: the softmax makes the weights
-            // of the tokens that see it NaN, the others' products stay as they are
+            // of the tokens that see it NaN, the others' products stay as they are.  (The V ring is all that
+            // P V reads; a NaN in the other blocks only reaches logits, of hidden keys masked ones.)
             uint32_t poison = 0u;
             for (int r8 = 0; r8 < kKeysPerWarp; ++r8) {
               const int r = warp * kKeysPerWarp + r8;
               if (base + r <= x.tok0 || base + r >= x.hi) continue;
-              bool found = false;
+              // 32 pieces of 16 bytes: the row's 256 values of this half
+              uint4* at = reinterpret_cast<uint4*>(v_st + (lane >> 3) * K_CHUNK + r * 128 + ((lane & 7) << 4));
+              const uint4 y = *at;
+              uint32_t w[4] = {y.x, y.y, y.z, y.w};
+              bool f = false;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {  // 64 pieces of 16 bytes: the 512 values
-                const int i = lane + 32 * e;
-                uint4* at = reinterpret_cast<uint4*>(stage + (i >> 3) * K_CHUNK + r * 128 + ((i & 7) << 4));
-                uint4 y = *at;
-                uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                bool f = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; f = true; }
-                  if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; f = true; }
-                }
-                if (f) *at = make_uint4(w[0], w[1], w[2], w[3]);
-                found |= f;
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; f = true; }
+                if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; f = true; }
               }
-              if (__any_sync(0xFFFFFFFFu, found)) poison |= 1u << r8;
+              if (f) *at = make_uint4(w[0], w[1], w[2], w[3]);
+              if (__any_sync(0xFFFFFFFFu, f)) poison |= 1u << r8;
             }
-            if (lane == 0) poisons[s * 8 + warp] = (uint8_t)poison;
+            if (lane == 0) poisons[slot * 8 + warp] = (uint8_t)poison;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_full[s]);
@@ -635,23 +697,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (u == last_u) {
-        // the CTA's last unit: columns [64, 128) and [128, 256) of O_v / l, staged in the ring (free after the last P V)
+        // the CTA's last unit: columns [64, 128) and [128, 256) of O_v / l, staged in the V ring (free after the last P V)
         if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
         tc_fence_after();
-        store_o(p, x, my_lanes, quarter, part ? 128 : 64, part ? 256 : 128, k_ring + warp * 4096, stats[quarter * 32 + lane], ntiles > 0);
+        store_o(p, x, my_lanes, quarter, part ? 128 : 64, part ? 256 : 128, smem + OFF_V + warp * 4096, stats[quarter * 32 + lane], ntiles > 0);
         tc_fence_before();
       }
     }
-    if (!ok && tid == 0) {
-      // gave up: copies in flight must land before the CTA exits
-      if (staged >= 1) mbar_wait(&q_stage[0], ui & 1, p.err, nullptr);
-      if (staged >= 2) mbar_wait(&q_stage[1], ui & 1, p.err, nullptr);
-    }
+    // gave up: copies in flight must land before the CTA exits
+    if (!ok && staged) mbar_wait(q_stage, ui & 1, p.err, nullptr);
     if (!ok && !kQuant && lane == 0) {
-      for (int t = gi; t >= 0 && t > gi - kStages; --t)
-        if (t < gi) mbar_wait(&k_full[t % kStages], (uint32_t)((t / kStages) & 1), p.err, nullptr);
-      for (int i = 0; i < kStages; ++i)
-        if (nland[i]) mbar_wait(&land[i], (nland[i] - 1) & 1, p.err, nullptr);
+      for (int t = gi - 1; t <= gi; ++t)
+        if (t >= 0) mbar_wait(&k_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr);
+      for (int i = 0; i < 2; ++i) mbar_wait(&land[i], nland[i] & 1, p.err, nullptr);
     }
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------------ Q K^T
@@ -671,21 +729,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       for (int j = 0; j < ntiles; ++j, ++gi) {
-        const int s = gi % kStages;
-        if (!(ok = warp_wait(&k_full[s], (gi / kStages) & 1, p.err, abort_flag))) break;
+        const int s = gi & 1;
+        if (!(ok = warp_wait(&k_full[s], (gi / 2) & 1, p.err, abort_flag))) break;
         if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
         tc_fence_after();
-        const uint64_t kd = sw128_desc(smem_u32(k_ring + s * K_BYTES), 16, 1024);
+        const uint64_t xd = sw128_desc(smem_u32(smem + OFF_X), 16, 1024);
+        const uint64_t yd = sw128_desc(smem_u32(smem + OFF_Y + gi % kYStages * kYBlocks * K_CHUNK), 16, 1024);
+        const uint64_t vd = sw128_desc(smem_u32(smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK), 16, 1024);
         constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
         if (elect_one()) {
-          umma_ts<0>(d_s, a_q, kd, idesc_s);
+          // place i / 4 of the block order, 16 dims (32 bytes, 8 tensor-memory columns) each
+          umma_ss<0>(d_s, qd, xd, idesc_s);
 #pragma unroll
-          for (int i = 1; i < 4 * kTmemQChunks; ++i)
-            umma_ts<1>(d_s, a_q + (uint32_t)(i * 8), kd + (uint64_t)(i >> 2) * kc + (uint64_t)(i & 3) * 2, idesc_s);
-#pragma unroll
-          for (int i = 0; i < 4 * (kChunks - kTmemQChunks); ++i)
-            umma_ss<1>(d_s, qd + (uint64_t)(i >> 2) * qc + (uint64_t)(i & 3) * 2,
-                       kd + (uint64_t)(kTmemQChunks + (i >> 2)) * kc + (uint64_t)(i & 3) * 2, idesc_s);
+          for (int i = 1; i < 4 * kChunks; ++i) {
+            const int c = i >> 2;
+            const uint64_t bd = (c < 2 ? xd + (uint64_t)c * kc : c < 5 ? yd + (uint64_t)(c - 2) * kc : vd + (uint64_t)(c - 5) * kc) +
+                                (uint64_t)(i & 3) * 2;
+            if (c < kSmemQ)
+              umma_ss<1>(d_s, qd + (uint64_t)c * qc + (uint64_t)(i & 3) * 2, bd, idesc_s);
+            else
+              umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), bd, idesc_s);
+            if (i == 4 * kXBlocks - 1) mma_commit(x_empty);
+            if (i == 4 * (kXBlocks + kYBlocks) - 1) mma_commit(&y_empty[gi % kYStages]);
+          }
           mma_commit(s_full);
           if (j == ntiles - 1) mma_commit(q_empty);
         }
@@ -707,10 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!x.rows) continue;
       const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
       for (int j = 0; j < ntiles; ++j, ++gi) {
-        const int s = gi % kStages;
         if (!(ok = warp_wait(p_full, gi & 1, p.err, abort_flag))) break;
         tc_fence_after();
-        const uint64_t vd = sw128_desc(smem_u32(k_ring + s * K_BYTES) + (uint32_t)(x.v * 4 * K_CHUNK), K_CHUNK, 1024);
+        const uint64_t vd = sw128_desc(smem_u32(smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK), K_CHUNK, 1024);
         if (elect_one()) {
           if (j > 0)
             umma_ss<1>(d_o, pd, vd, idesc_o);
@@ -720,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
           umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
           mma_commit(pv_done);
-          mma_commit(&k_empty[s]);
+          mma_commit(&v_empty[gi % kVStages]);
         }
         __syncwarp();
       }
@@ -747,43 +812,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         limit = r < x.rows ? x.tok0 + (x.h0 + r) / p.H : -1;
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < ntiles; ++j, ++gi) {
-        const int s = gi % kStages;
+        const int slot = gi % kMaskSlots;
         if (!(ok = warp_wait(s_full, gi & 1, p.err, abort_flag))) break;
-        if (!(ok = warp_wait(&k_full[s], (gi / kStages) & 1, p.err, abort_flag))) break;  // (long past: orders the masks)
+        if (!(ok = warp_wait(&k_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;  // (long past: orders the masks)
         tc_fence_after();
         uint32_t sv[64];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_S + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
-        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + s * 8);
-        const uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + s * 8);
+        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + slot * 8);
+        const uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * 8);
         const int d = limit - (x.lo + j * kTile);  // this row sees the tile's keys 0 .. d
         if (d < 63) valid &= d < 0 ? 0ull : (2ull << d) - 1ull;
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty);
-        float mt = -INFINITY;
-        if (__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
+        if (!__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) {
-            const float xv = __uint_as_float(sv[c]) * p.scale_log2;
-            sv[c] = __float_as_uint(xv);
-            mt = fmaxf(mt, xv);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float xv = ((poison >> c) & 1u) ? __uint_as_float(0x7FC00000u) : __uint_as_float(sv[c]) * p.scale_log2;
-            xv = ((valid >> c) & 1u) ? xv : -INFINITY;
-            sv[c] = __float_as_uint(xv);
-            mt = fmaxf(mt, xv);
+            if ((poison >> c) & 1u) sv[c] = 0x7FC00000u;
+            if (!((valid >> c) & 1u)) sv[c] = 0xFF800000u;
           }
         }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(sv[c]);
+#pragma unroll
+        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         if (gi >= 1 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
-        // Lazy rescale: the base m_used moves only when some row's maximum exceeds it by more than 2^8
-        // (P stays <= 256), for the whole warp since the tensor-memory accesses are warp-collective.
+        // Lazy rescale: a row's base m_used moves only when its maximum exceeds it by more than 2^8 (P stays
+        // <= 256); the warp takes the step together, since the tensor-memory accesses are warp-collective.
         if (__any_sync(0xFFFFFFFFu, mt > m_used + 8.0f)) {
-          const float m_new = fmaxf(m_used, mt);
+          const float m_new = mt > m_used + 8.0f ? mt : m_used;  // (a row's base depends on that row alone)
           const float f = m_new == -INFINITY ? 1.0f : exp2f(m_used - m_new);  // 0 when m_used = -inf
           if (j > 0) {
             tc_fence_after();
@@ -803,20 +864,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           m_used = m_new;
         }
-        float psum = 0.0f;
         uint32_t pk[32];
-        const float msub = m_used == -INFINITY ? 0.0f : m_used;
+        const float nsub = m_used == -INFINITY ? 0.0f : -m_used;
+        float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), ns2 = make_float2(nsub, nsub);
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
-          const float p0 = fast_exp2(__uint_as_float(sv[c]) - msub);
-          const float p1 = fast_exp2(__uint_as_float(sv[c + 1]) - msub);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-          // the normaliser sums the rounded weights that P V uses
-          const float2 bf = __bfloat1622float2(b);
-          psum += bf.x + bf.y;
+          const float2 e = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, ns2);
+          const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+          // (the normaliser sums the weights before their rounding to bf16, which P V needs)
+          ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], w);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
           pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        l += psum;
+        const float2 pt = add2(ps[0], ps[1]);
+        l += pt.x + pt.y;
         uint8_t* prow = p_s + (r >> 3) * 1024 + (r & 7) * 16;
 #pragma unroll
         for (int kc = 0; kc < 8; ++kc)
