@@ -28,10 +28,11 @@
 // significant bits and its scale is a power of two) and store them in the swizzled layout.  bf16
 // latents come by TMA: whole 64-token pages as nine 64-row boxes, a page's visible part by gather4.
 //
-// Roles (14 warps): 0-7 fill the rings and move Q into tensor memory (staged by TMA through idle
-// ring blocks at the start of a unit); 8 issues Q K^T, 9 issues P V (each the whole warp, so that the
-// compiler keeps the issue uniform: with elect.sync one M = 128, N = 64 product is issued every ~32
-// cycles, against ~60 from a thread chosen by its index); 10-13 softmax and epilogue, one row per thread.
+// Roles (16 warps): 0-7 fill the rings and move Q into tensor memory (staged by TMA through idle
+// ring blocks at the start of a unit); 8-11 softmax and epilogue, one row per thread; 12 issues the
+// products (the whole warp, so that the compiler keeps the issue uniform: with elect.sync one M = 128, N = 64
+// product is issued every ~32 cycles, against ~60 from a thread chosen by its index); 13 looks the
+// keys' pool rows up, a few tiles ahead.
 // All waits are bounded; bad rows set the device error word and are skipped.
 #include <cuda.h>
 #include <math.h>
@@ -49,8 +50,6 @@ constexpr int kChunks = 9;               // 64-dim column blocks of a row
 constexpr int kSmemQ = 3;                // Q blocks in shared memory (the first that Q K^T uses), the rest in tensor memory
 constexpr int kFillWarps = 8;
 constexpr int kKeysPerWarp = kTile / kFillWarps;  // 8
-constexpr int kQkWarp = 8, kPvWarp = 9, kSoftmaxWarp = 10;
-constexpr int kThreads = 32 * 14;
 constexpr int kLatentBytes = 640;        // data bytes of a quantised row
 
 // A tile's blocks in the order Q K^T uses them: X0 (RoPE), X1, Y0, Y1, Y2 (the values of the other
@@ -70,13 +69,17 @@ constexpr int OFF_Y = OFF_P + kRows * kTile * 2;
 constexpr int OFF_X = OFF_Y + kYStages * kYBlocks * K_CHUNK;
 constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;
 constexpr int OFF_BAR = OFF_V + kVStages * kVBlocks * K_CHUNK;
-constexpr int NBAR = 24;
+constexpr int NBAR = 32;
 constexpr int kMaskSlots = 4;
 constexpr int OFF_MASK = OFF_BAR + NBAR * 8;             // [slot] 64-bit mask of real rows (a byte per warp)
 constexpr int OFF_POISON = OFF_MASK + kMaskSlots * 8;    // [slot] rows with NaN or infinity, see below
-constexpr int OFF_MISC = OFF_POISON + kMaskSlots * 8;
-constexpr int OFF_STATS = OFF_MISC + 32;                 // 1 / l of each row (last unit)
-constexpr int SMEM = OFF_STATS + kRows * 4 + 1024;
+constexpr int kRowSlots = 4;
+constexpr int OFF_STATS = OFF_POISON + kMaskSlots * 8;   // 1 / l of each row (last unit)
+constexpr int OFF_MISC = OFF_STATS + kRows * 4;
+constexpr int OFF_ROWS = OFF_MISC + 32;                  // quantised: [slot][64] pool row of each key of a tile, -1: none to see;
+                                                         // bf16: [slot] page of the tile, then [2][2][128] row maxima exchanged
+constexpr int SMEM = OFF_ROWS + kRowSlots * 4 + 2 * 2 * kRows * 4;
+static_assert(kRowSlots * kTile * 4 <= 2 * 2 * kRows * 4, "row ring");
 static_assert(SMEM <= 232448, "shared memory budget");
 static_assert(kYStages * kYBlocks * K_CHUNK == 3 * Q_CHUNK && kXBlocks * K_CHUNK == Q_CHUNK && kVBlocks * K_CHUNK == 2 * Q_CHUNK,
               "six Q blocks are staged in the Y and X rings and one V stage");
@@ -88,6 +91,20 @@ enum Source {
   kSelected,   // quantised rows chosen per query by idx (or every visible position)
   kPages,      // quantised rows at consecutive positions
   kPagesBf16,  // bf16 rows at consecutive positions
+};
+
+// Warps by source: 0-7 fill; softmax, `kParts` warps per 32 rows (bf16 tiles come fast enough that one warp's
+// softmax, a chain of ~2100 cycles, would set the pace); one to issue products, one to look pages up, two idle
+// ones to complete the warpgroup.  Registers a thread by warpgroup, within what the block was launched with:
+// quantised 2 x 136 + 136 + 104 = 4 x 128, bf16 2 x 80 + 2 x 104 + 104 <= 5 x 96.  (Spilled registers cost more than
+// elsewhere: they miss the small L1 left beside 227 KB of shared memory.)
+template <Source kSrc>
+struct Roles {
+  static constexpr bool kQuant = kSrc != kPagesBf16;
+  static constexpr int kParts = kQuant ? 1 : 2;
+  static constexpr int kSoftmaxWarp = kFillWarps, kIssueWarp = kFillWarps + 4 * kParts, kLookupWarp = kIssueWarp + 1;
+  static constexpr int kThreads = 32 * (kIssueWarp + 4);
+  static constexpr int kFillRegs = kQuant ? 136 : 80, kSoftmaxRegs = kQuant ? 136 : 104, kIssueRegs = 104;
 };
 
 struct Params {
@@ -117,6 +134,11 @@ struct Unit {
   int v;
 };
 
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error ~2^-22; 2^-inf = 0
@@ -126,6 +148,24 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// 16-byte cp.async past L1; bytes from `size` (0 or 16) on are zeros
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+
+// Loads that stay where they are written: left to itself the compiler moves the loads of the next tile down to
+// their use, a tile later, and with them their whole latency.
+__device__ __forceinline__ uint4 load16_here(const void* a) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ float loadf_here(const float* a) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(a));
+  return v;
 }
 
 // two f32 operations in one instruction
@@ -239,7 +279,7 @@ __device__ __forceinline__ Unit get_unit(const Params& p, int u, int* err) {
   return x;
 }
 
-// Eight codes (two words) times a power of two, as four bf16 pairs: the code's exponent and mantissa
+// Codes times a power of two, as four bf16 pairs: the code's exponent and mantissa
 // are moved to a bf16's, whose value is then the code's times 2^-120 (subnormal codes become
 // subnormal bf16), and one exact product by 2^(e + 120) does the rest; `m2` (1 unless e > 7, where 2^(e + 120) is
 // no bf16) takes what is left.
@@ -254,58 +294,58 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t m, uint32_t& lo, ui
   hi = mul_bf16x2(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), m);
 }
 
-// O_v / l of this warp's 32 rows, columns [c_lo, c_hi) (multiples of 64), from tensor memory to the
-// partials (f32) or the output (bf16) through a 4 KB staging area: lane i stages its row's 128-byte block
-// with its 16-byte pieces permuted, then the warp writes whole 128-byte pieces of four rows at a time.
+// O_v / l of this warp's 32 rows, columns [c_lo, c_hi) (multiples of 32), from tensor memory to the
+// partials (f32) or the output (bf16) through a 2 KB staging area: lane i stages 64 bytes of its row, its
+// 16-byte pieces permuted against bank conflicts, then the warp writes whole 64-byte pieces of eight rows at a time.
 __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t lane_base, int quarter, int c_lo, int c_hi,
                                         uint8_t* stage, float inv, bool have_o) {
   const int lane = threadIdx.x & 31;
-  const int srow = lane >> 3, spiece = lane & 7;
   const bool f32out = p.nsplit > 1;
   const int rows = min(32, x.rows - quarter * 32);
+  uint8_t* mine = stage + lane * 64;
+  const int mix = (lane >> 1) & 3;
   auto flush = [&](int col) {
     __syncwarp();
 #pragma unroll
-    for (int k4 = 0; k4 < 8; ++k4) {
-      const int rr = k4 * 4 + srow;
-      const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((spiece ^ (rr & 7)) << 4));
+    for (int k = 0; k < 4; ++k) {
+      const int rr = k * 8 + (lane >> 2), piece = lane & 3;
+      const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
       if (rr < rows) {
         if (f32out)
-          *reinterpret_cast<uint4*>(p.part_o + ((int64_t)x.prow + quarter * 32 + rr) * kDv + x.v * kHalf + col + spiece * 4) = y;
+          *reinterpret_cast<uint4*>(p.part_o + ((int64_t)x.prow + quarter * 32 + rr) * kDv + x.v * kHalf + col + piece * 4) = y;
         else
-          *reinterpret_cast<uint4*>(p.out + ((int64_t)x.row0 + quarter * 32 + rr) * kDv + x.v * kHalf + col + spiece * 8) = y;
+          *reinterpret_cast<uint4*>(p.out + ((int64_t)x.row0 + quarter * 32 + rr) * kDv + x.v * kHalf + col + piece * 8) = y;
       }
     }
     __syncwarp();
   };
   if (rows <= 0) return;
 #pragma unroll 1
-  for (int c0 = c_lo; c0 < c_hi; c0 += 64) {
-    uint32_t o[64];
+  for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+    uint32_t o[32];
     if (have_o) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_O + c0 + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
+      for (int c = 0; c < 2; ++c) tmem_ld16(lane_base + TM_O + c0 + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
       tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) o[c] = 0u;
+      for (int c = 0; c < 32; ++c) o[c] = 0u;
     }
-    uint8_t* mine = stage + lane * 128;
     if (f32out) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = 32 * b + 4 * j;
-          *reinterpret_cast<float4*>(mine + ((j ^ (lane & 7)) << 4)) =
+        for (int j = 0; j < 4; ++j) {
+          const int c = 16 * b + 4 * j;
+          *reinterpret_cast<float4*>(mine + ((j ^ mix) << 4)) =
               make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv, __uint_as_float(o[c + 2]) * inv,
                           __uint_as_float(o[c + 3]) * inv);
         }
-        flush(c0 + 32 * b);
+        flush(c0 + 16 * b);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -313,7 +353,7 @@ __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t
               __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
           pk[e] = *reinterpret_cast<const uint32_t*>(&hv);
         }
-        *reinterpret_cast<uint4*>(mine + ((j ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(mine + ((j ^ mix) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
       flush(c0);
     }
@@ -321,12 +361,17 @@ __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t
 }
 
 template <Source kSrc>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
     mla_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
                       const __grid_constant__ CUtensorMap pmap, const Params p) {
-  constexpr bool kQuant = kSrc != kPagesBf16;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using R = Roles<kSrc>;
+  constexpr bool kQuant = R::kQuant;
+  constexpr int kParts = R::kParts, kIssueWarp = R::kIssueWarp;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // (swizzled blocks need it; the whole of shared memory starts there)
+    if (threadIdx.x == 0) raise_error(p.err, DSA_DEVERR_TIMEOUT);
+    return;
+  }
   uint8_t* q_s = smem + OFF_Q;
   uint8_t* p_s = smem + OFF_P;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -343,9 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_empty = bars + 15;
   uint64_t* p_full = bars + 16;
   uint64_t* pv_done = bars + 17;
-  uint64_t* fin = bars + 18;        // both issuing warps' products have completed
+  uint64_t* fin = bars + 18;        // every product has completed
   uint64_t* ep_last = bars + 19;    // last unit: 1 / l published after its last P V
+  uint64_t* r_full = bars + 20;     // [kRowSlots] pool rows of a tile looked up
+  uint64_t* r_empty = bars + 24;    // [kRowSlots] ... read by the fill warps
   uint8_t* masks = smem + OFF_MASK;
+  int32_t* row_ring = reinterpret_cast<int32_t*>(smem + OFF_ROWS);
+  float* row_max = reinterpret_cast<float*>(smem + OFF_ROWS + kRowSlots * 4);
+  uint64_t* x_bar = bars + 28;      // [4] the two softmax warps of 32 rows have exchanged their maxima
   uint8_t* poisons = smem + OFF_POISON;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
@@ -360,6 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_full[i], kFillWarps);
       mbar_init(&land[i], kFillWarps);
     }
+    for (int i = 0; i < kRowSlots; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_empty[i], kFillWarps);
+    }
     mbar_init(x_empty, 1);
     for (int i = 0; i < kYStages; ++i) mbar_init(&y_empty[i], 1);
     for (int i = 0; i < kVStages; ++i) mbar_init(&v_empty[i], 1);
@@ -368,15 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, 32 * kFillWarps);
     mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(s_empty, 4);
-    mbar_init(p_full, 128);
+    mbar_init(s_empty, 4 * kParts);
+    mbar_init(p_full, 128 * kParts);
     mbar_init(pv_done, 1);
-    mbar_init(fin, 2);
-    mbar_init(ep_last, 128);
+    mbar_init(fin, 1);
+    mbar_init(ep_last, 128 * kParts);
+    for (int i = 0; i < 4; ++i) mbar_init(&x_bar[i], 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kQkWarp) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tmem_slot, TM_COLS);
     tmem_relinquish();
   }
@@ -388,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the CTA's last unit that has work (its epilogue is shared among the warps)
   int last_u = -1;
-  if (warp < kFillWarps || warp >= kSoftmaxWarp) {
+  if (warp < kIssueWarp) {
     for (int u = blockIdx.x + (units - 1 - (int)blockIdx.x) / (int)gridDim.x * (int)gridDim.x; u >= 0; u -= gridDim.x)
       if (get_unit<kSrc>(p, u, nullptr).rows) {
         last_u = u;
@@ -397,10 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp < kFillWarps) {
+    if constexpr (kQuant)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kFillRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kFillRegs));
     // ------------------------------------------------------------------ rings and Q
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const int half = lane >> 4, l16 = lane & 15;  // quantised rows: two at a time, 16 lanes each
+    const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // quantised rows: two at a time, 16 lanes each
     int gi = 0, ui = 0;
     uint32_t nland[2] = {0u, 0u};
     bool ok = true, staged = false;
@@ -410,89 +469,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
       const bool report = x.v == 0;
 
-      // --- row lookup, pipelined so that no loaded value is looked at in the tile that loads it.
-      // kSelected: lane j < 8 has key 8 warp + j of a tile: selected position two tiles ahead, page
-      // table entry one tile ahead.  kPages*: every lane has the tile's page table entry.
-      auto load_slot = [&](int j) -> int {
-        const int slot = x.lo + j * kTile + warp * kKeysPerWarp + lane;
-        if (lane >= kKeysPerWarp || j >= ntiles || slot >= x.hi) return -1;
-        return p.idx ? p.idx[(int64_t)(x.row0 / p.H) * p.k + slot] : slot;
-      };
-      auto load_page = [&](int lblk) -> int {
-        return lblk < p.max_blocks ? p.block_table[(int64_t)x.req * p.max_blocks + lblk] : -1;
-      };
-      auto visible = [&](int ps) { return x.req >= 0 && ps >= 0 && ps <= x.tok0; };
-      int ps0 = -1, ps1 = -1, blk0 = -1, blk1 = -1;  // of the tile whose rows are looked up next, and the one after
-      if constexpr (kSrc == kSelected) {
-        ps0 = load_slot(0);
-        ps1 = load_slot(1);
-        if (visible(ps0)) blk0 = load_page(ps0 / kTile);
-      } else {
-        blk0 = load_page(x.lo / kTile);
-        if (ntiles > 1) blk1 = load_page(x.lo / kTile + 1);
-      }
-      // pool row of this lane's key of tile j (kSelected: lanes 0 .. 7, else key 8 warp + lane % 8), -1
-      // when there is none to see; called for j = 0, 1, 2, ...
-      auto next_row = [&](int j) -> int {
-        int row = -1;
-        if (kSrc == kSelected) {
-          if (visible(ps0)) {
-            if (blk0 >= 0 && blk0 < p.num_blocks)
-              row = blk0 * kTile + ps0 % kTile;
-            else if (report)
-              raise_error(p.err, DSA_DEVERR_BLOCK_ID);
-          } else if (ps0 != -1 && x.req >= 0 && report) {
-            raise_error(p.err, DSA_DEVERR_INDEX);
-          }
-          ps0 = ps1;
-          ps1 = load_slot(j + 2);
-          blk0 = visible(ps0) ? load_page(ps0 / kTile) : -1;
-        } else if (j < ntiles) {
-          const int r = warp * kKeysPerWarp + (lane & 7);
-          if (blk0 >= 0 && blk0 < p.num_blocks) {
-            if (x.lo + j * kTile + r < x.hi) row = blk0 * kTile + r;
-          } else if (report) {
-            raise_error(p.err, DSA_DEVERR_BLOCK_ID);
-          }
-          blk0 = blk1;
-          if (j + 2 < ntiles) blk1 = load_page(x.lo / kTile + j + 2);
-        }
-        return row;
-      };
+      // pool row of key `key` of this warp's eight, of CTA tile g (r_full of that tile has been waited for)
+      auto row_of = [&](int g, int key) -> int { return row_ring[g % kRowSlots * kTile + warp * kKeysPerWarp + key]; };
+      auto wait_rows = [&](int g) { return warp_wait(&r_full[g % kRowSlots], (g / kRowSlots) & 1, p.err, abort_flag); };
 
       // --- quantised rows in flight: pair q is the rows 8 warp + 2 q + half; a lane has 16 of its codes in
-      // this CTA's value half (hh = 0) and 16 in the other (hh = 1)
-      uint4 code[4][2], rope[2];
-      float sc[4][2];
-      auto load_codes = [&](int rw, int q, int hh) {
-        const int row = __shfl_sync(0xFFFFFFFFu, rw, 2 * q + half);
-        const int vh = hh ^ x.v;
-        code[q][hh] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0) code[q][hh] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + 256 * vh) + l16);
-      };
-      auto load_scales = [&](int rw, int q) {
-        const int row = __shfl_sync(0xFFFFFFFFu, rw, 2 * q + half);
-        sc[q][0] = sc[q][1] = 1.0f;
-        if (row >= 0) {
-          sc[q][0] = __ldg(p.scale + (int64_t)row * 4 + 2 * x.v + (l16 >> 3));
-          sc[q][1] = __ldg(p.scale + (int64_t)row * 4 + 2 * (1 - x.v) + (l16 >> 3));
-        }
-      };
-      auto load_rope = [&](int rw, int i) {
-        const int row = __shfl_sync(0xFFFFFFFFu, rw, 4 * i + (lane >> 3));
-        rope[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0) rope[i] = __ldg(reinterpret_cast<const uint4*>(p.data + (int64_t)row * kLatentBytes + kDv) + (lane & 7));
-      };
-      int row_n = next_row(0);  // rows of the tile in registers (quantised) or about to be copied
-      if constexpr (kQuant) {
+      // this CTA's value half (hh = 0) and 16 in the other (hh = 1).  Lane l has the scale of row l / 4, group
+      // l % 4, of the warp's eight rows.  Loads of one kind are issued together, as far as possible ahead of
+      // their use: a warp waits for loads by a handful of counters, so waiting for an old load can mean waiting
+      // for a young one that shares its counter.  None is conditional (a key without a row reads row 0).
+      uint4 code[4][2];
+      float sc = 1.0f;
+      uint32_t seen = 0u, bad = 0u;  // of the tile in registers: keys with a row; lanes with no row or no power of two
+      bool all_plain = true;
+      auto load_codes = [&](int g, int hh) {
+        const uint8_t* base = p.data + 256 * (hh ^ x.v) + 16 * l16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          load_scales(row_n, q);
-          load_codes(row_n, q, 0);
-          load_codes(row_n, q, 1);
-        }
-        load_rope(row_n, 0);
-        load_rope(row_n, 1);
+        for (int q = 0; q < 4; ++q) code[q][hh] = load16_here(base + (int64_t)max(0, row_of(g, 2 * q + half)) * kLatentBytes);
+      };
+      auto load_scales = [&](int g) -> float { return loadf_here(p.scale + (int64_t)max(0, row_of(g, lane >> 2)) * 4 + (lane & 3)); };
+      auto check_rows = [&](int g) {
+        const bool none = row_of(g, lane >> 2) < 0;
+        bad = __ballot_sync(0xFFFFFFFFu, none || !latent_scale_ok(sc));
+        seen = ~__ballot_sync(0xFFFFFFFFu, none);
+        all_plain = bad == 0u && !__any_sync(0xFFFFFFFFu, sc > 128.0f);
+      };
+      if (kQuant && ntiles > 0) {
+        if (!(ok = wait_rows(gi))) break;
+        sc = load_scales(gi);
+        load_codes(gi, 0);
+        load_codes(gi, 1);
+        check_rows(gi);
       }
 
       // --- Q of the unit, once the unit before is past its last Q K^T: places 0 .. 2 of the order to
@@ -541,90 +548,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* v_st = smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK;
         uint8_t* y_st = smem + OFF_Y + gi % kYStages * kYBlocks * K_CHUNK;
         uint8_t* x_st = smem + OFF_X;
-        const int row = row_n;
-        row_n = next_row(j + 1);
         auto wait_v = [&]() { return gi < kVStages || warp_wait(&v_empty[gi % kVStages], ((gi / kVStages) - 1) & 1, p.err, abort_flag); };
         auto wait_y = [&]() { return gi < kYStages || warp_wait(&y_empty[gi % kYStages], ((gi / kYStages) - 1) & 1, p.err, abort_flag); };
         auto wait_x = [&]() { return gi < 1 || warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag); };
         if constexpr (kQuant) {
-          const uint32_t seen = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
-          uint32_t valid = seen, poison = 0u;
-          uint32_t drop = 0u;  // bit q: this lane's row of pair q has scales that are no powers of two
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc[q][0]) || !latent_scale_ok(sc[q][1]));
-            if (bad) {
-              valid &= ~(((bad & 0xFFFFu ? 1u : 0u) | (bad >> 16 ? 2u : 0u)) << (2 * q));
-              if (half ? bad >> 16 : bad & 0xFFFFu) drop |= 1u << q;
-            }
-          }
-          // 16 codes into the row's blocks: `dst` is the row of the lane's 64-dim block, pieces 2 (l16 % 4) and
-          // the next; the two rows of a pair differ in bit 0, so a store covers all eight bank groups
           uint32_t nan[4] = {0u, 0u, 0u, 0u};
-          auto put = [&](int q, int hh, uint8_t* dst, int r) {
+          // 16 codes into the row's blocks: `dst` is the row of the lane's 64-dim block, pieces 2 (l16 % 4) and
+          // the next; eight consecutive lanes hold four pieces of both rows of a pair, which differ in bit 0, so
+          // they store to all eight bank groups.  kPlain: every key has a row, and scales are at most 2^7.
+          auto put = [&](auto plain, int q, int hh, uint8_t* dst) {
+            constexpr bool kPlain = decltype(plain)::value;
+            const int r = warp * kKeysPerWarp + 2 * q + half;
             uint32_t w[4] = {code[q][hh].x, code[q][hh].y, code[q][hh].z, code[q][hh].w};
-            const uint32_t e = __float_as_uint(sc[q][hh]) >> 23;  // biased exponent of the scale
-            // 2^(e - 127 + 120) as a bf16 pair, at most 2^127; what is left above that is m2 below
-            const uint32_t e1 = min(e + 120u, 254u);
-            const uint32_t m1 = e1 << 7 | e1 << 23;
-            if (drop) {
-              if ((drop >> q) & 1u) w[0] = w[1] = w[2] = w[3] = 0u;
-            }
+            const float my_sc = __shfl_sync(0xFFFFFFFFu, sc, (2 * q + half) * 4 + 2 * (hh ^ x.v) + (l16 >> 3));
+            // 2^(e - 127 + 120) as a bf16 pair (e: the scale's biased exponent), at most 2^127; m2: the rest
+            const uint32_t e = __float_as_uint(my_sc) >> 23, e1 = kPlain ? e + 120u : min(e + 120u, 254u);
+            const uint32_t m1 = e1 * 0x00800080u;
+            if (!kPlain && ((bad >> (4 * (2 * q + half))) & 0xFu)) w[0] = w[1] = w[2] = w[3] = 0u;
             uint32_t b[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               nan[q] |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: that code is NaN
               decode4(w[i], m1, b[2 * i], b[2 * i + 1]);
             }
-            if (e > 134u) {  // scales above 2^7
-              const uint32_t e2 = min(e, 246u) - 134u + 127u;
-              const uint32_t m2 = e2 << 7 | e2 << 23;
+            if (!kPlain && e > 134u) {
+              const uint32_t m2 = (min(e, 246u) - 134u + 127u) * 0x00800080u;
 #pragma unroll
               for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(b[i], m2);
             }
             const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
-            *reinterpret_cast<uint4*>(dst + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
-            *reinterpret_cast<uint4*>(dst + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
+          };
+          auto put4 = [&](int hh, uint8_t* dst) {
+            if (all_plain) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) put(Flag<true>(), q, hh, dst);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) put(Flag<false>(), q, hh, dst);
+            }
           };
           if (!(ok = wait_v())) break;
-          uint8_t* v_dst = v_st + (l16 >> 2) * K_CHUNK;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = warp * kKeysPerWarp + 2 * q + half;
-            put(q, 0, v_dst + r * 128, r);
-            load_codes(row_n, q, 0);
+          put4(0, v_st + (l16 >> 2) * K_CHUNK);
+          const bool more = j + 1 < ntiles;
+          float sc_n = 1.0f;
+          if (more) {
+            if (!(ok = wait_rows(gi + 1))) break;
+            sc_n = load_scales(gi + 1);
+            load_codes(gi + 1, 0);
           }
           if (!(ok = wait_y()) || !(ok = wait_x())) break;
-          uint8_t* o_dst = (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = warp * kKeysPerWarp + 2 * q + half;
-            put(q, 1, o_dst + r * 128, r);
-            load_codes(row_n, q, 1);
-            load_scales(row_n, q);
-            const uint32_t np = __ballot_sync(0xFFFFFFFFu, (nan[q] & 0x80808080u) != 0u);
-            poison |= (((np & 0xFFFFu) ? 1u : 0u) | ((np >> 16) ? 2u : 0u)) << (2 * q);
-          }
+          // the RoPE part as it is, in the background (zeros for a row that is not there)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r8 = 4 * i + (lane >> 3);
             const int r = warp * kKeysPerWarp + r8;
-            *reinterpret_cast<uint4*>(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
-                (valid >> r8) & 1u ? rope[i] : make_uint4(0u, 0u, 0u, 0u);
-            load_rope(row_n, i);
+            cp_async_16(smem_u32(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
+                        p.data + (int64_t)max(0, row_of(gi, r8)) * kLatentBytes + kDv + 16 * (lane & 7),
+                        ((bad >> (4 * r8)) & 0xFu) ? 0u : 16u);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&r_empty[gi % kRowSlots]);
+          put4(1, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK);
+          uint32_t nan_rows = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) nan_rows |= (nan[q] & 0x80808080u) ? 1u << (2 * q + half) : 0u;
+          const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
           if (lane == 0) {
+            uint32_t valid = 0xFFu;
+            if (bad) {
+              bool flag = false;
+              for (int r8 = 0; r8 < kKeysPerWarp; ++r8)
+                if ((bad >> (4 * r8)) & 0xFu) {
+                  valid &= ~(1u << r8);
+                  flag |= (seen >> (4 * r8)) & 1u;
+                }
+              if (report && flag) raise_error(p.err, DSA_DEVERR_SCALE);
+            }
             masks[slot * 8 + warp] = (uint8_t)valid;
             poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
-            if (report && seen != valid) raise_error(p.err, DSA_DEVERR_SCALE);
           }
+          if (more) {
+            sc = sc_n;
+            check_rows(gi + 1);
+            load_codes(gi + 1, 1);
+          }
+          cp_async_wait_all();
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_full[s]);
         } else {
+          if (!(ok = wait_rows(gi))) break;
+          const int page = row_ring[gi % kRowSlots], key = warp * kKeysPerWarp + (lane & 7);
+          const int row = page >= 0 && x.lo + j * kTile + key < x.hi ? page * kTile + key : -1;
           const uint32_t valid = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
+          if (lane == 0) mbar_arrive(&r_empty[gi % kRowSlots]);
           const int base = x.lo + j * kTile;
-          const int prow0 = __shfl_sync(0xFFFFFFFFu, row, 0) - warp * kKeysPerWarp;  // the page's first row
           const bool whole = base + kTile <= x.hi && valid == 0xFFu;
           // rows that only some of the tile's tokens see: a NaN there must not reach the others through
           // 0 * NaN in P V.  They are looked over once they have landed, see below.
@@ -634,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto copy = [&](int lo, int hi, uint8_t* dst) {
             if (whole) {
               if (warp == 0 && lane == 0)
-                for (int c = lo; c < hi; ++c) tma_load_2d(dst + (c - lo) * K_CHUNK, &pmap, bar, block_of(c, x.v) * 64, prow0);
+                for (int c = lo; c < hi; ++c) tma_load_2d(dst + (c - lo) * K_CHUNK, &pmap, bar, block_of(c, x.v) * 64, page * kTile);
               return;
             }
 #pragma unroll
@@ -697,10 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (u == last_u) {
-        // the CTA's last unit: columns [64, 128) and [128, 256) of O_v / l, staged in the V ring (free after the last P V)
+        // the CTA's last unit: these warps store part of O_v / l too, staged in the V ring (free after the last P V)
         if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
         tc_fence_after();
-        store_o(p, x, my_lanes, quarter, part ? 128 : 64, part ? 256 : 128, smem + OFF_V + warp * 4096, stats[quarter * 32 + lane], ntiles > 0);
+        const int lo = kParts == 2 ? 64 + 128 * part : 64 + 96 * part;
+        store_o(p, x, my_lanes, quarter, lo, lo + (kParts == 2 ? 64 : 96), smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], ntiles > 0);
         tc_fence_before();
       }
     }
@@ -711,95 +732,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t >= 0) mbar_wait(&k_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr);
       for (int i = 0; i < 2; ++i) mbar_wait(&land[i], nland[i] & 1, p.err, nullptr);
     }
-  } else if (warp == kQkWarp) {
-    // ------------------------------------------------------------------ Q K^T
-    const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
-    const uint64_t qd = sw128_desc(smem_u32(q_s), 16, 1024);
-    const uint32_t d_s = tmem + TM_S, a_q = tmem + TM_Q;
-    int gi = 0, ui = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit x = get_unit<kSrc>(p, u, nullptr);
-      if (!x.rows) continue;
-      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
-      if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
-      ++ui;
-      if (ntiles == 0) {
-        if (elect_one()) mma_commit(q_empty);
-        __syncwarp();
-      }
-      for (int j = 0; j < ntiles; ++j, ++gi) {
-        const int s = gi & 1;
-        if (!(ok = warp_wait(&k_full[s], (gi / 2) & 1, p.err, abort_flag))) break;
-        if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
-        tc_fence_after();
-        const uint64_t xd = sw128_desc(smem_u32(smem + OFF_X), 16, 1024);
-        const uint64_t yd = sw128_desc(smem_u32(smem + OFF_Y + gi % kYStages * kYBlocks * K_CHUNK), 16, 1024);
-        const uint64_t vd = sw128_desc(smem_u32(smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK), 16, 1024);
-        constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
-        if (elect_one()) {
-          // place i / 4 of the block order, 16 dims (32 bytes, 8 tensor-memory columns) each
-          umma_ss<0>(d_s, qd, xd, idesc_s);
-#pragma unroll
-          for (int i = 1; i < 4 * kChunks; ++i) {
-            const int c = i >> 2;
-            const uint64_t bd = (c < 2 ? xd + (uint64_t)c * kc : c < 5 ? yd + (uint64_t)(c - 2) * kc : vd + (uint64_t)(c - 5) * kc) +
-                                (uint64_t)(i & 3) * 2;
-            if (c < kSmemQ)
-              umma_ss<1>(d_s, qd + (uint64_t)c * qc + (uint64_t)(i & 3) * 2, bd, idesc_s);
-            else
-              umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), bd, idesc_s);
-            if (i == 4 * kXBlocks - 1) mma_commit(x_empty);
-            if (i == 4 * (kXBlocks + kYBlocks) - 1) mma_commit(&y_empty[gi % kYStages]);
-          }
-          mma_commit(s_full);
-          if (j == ntiles - 1) mma_commit(q_empty);
-        }
-        __syncwarp();
-      }
-    }
-    if (elect_one()) mma_commit(fin);
-    __syncwarp();
-    mbar_wait(fin, 0, p.err, nullptr);
-  } else if (warp == kPvWarp) {
-    // ------------------------------------------------------------------ P V
-    const uint32_t idesc_o = idesc_f16(1u, 1u, (uint32_t)kRows, (uint32_t)kHalf);
-    const uint64_t pd = noswz_desc(smem_u32(p_s), 128, 1024);
-    const uint32_t d_o = tmem + TM_O;
-    int gi = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit x = get_unit<kSrc>(p, u, nullptr);
-      if (!x.rows) continue;
-      const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
-      for (int j = 0; j < ntiles; ++j, ++gi) {
-        if (!(ok = warp_wait(p_full, gi & 1, p.err, abort_flag))) break;
-        tc_fence_after();
-        const uint64_t vd = sw128_desc(smem_u32(smem + OFF_V + gi % kVStages * kVBlocks * K_CHUNK), K_CHUNK, 1024);
-        if (elect_one()) {
-          if (j > 0)
-            umma_ss<1>(d_o, pd, vd, idesc_o);
-          else
-            umma_ss<0>(d_o, pd, vd, idesc_o);
-          umma_ss<1>(d_o, pd + 16, vd + 128, idesc_o);
-          umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
-          umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
-          mma_commit(pv_done);
-          mma_commit(&v_empty[gi % kVStages]);
-        }
-        __syncwarp();
-      }
-    }
-    if (elect_one()) mma_commit(fin);
-    __syncwarp();
-    mbar_wait(fin, 0, p.err, nullptr);
-  } else {
+  } else if (warp < kIssueWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
     // ------------------------------------------------------------------ softmax and epilogue
-    const int quarter = warp & 3;
+    constexpr int kCols = kTile / kParts;  // keys of a tile, and columns of O_v in kHalf / kParts, of one warp
+    const int quarter = warp & 3, part = (warp - R::kSoftmaxWarp) >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    int gi = 0;
+    int gi = 0, nx = 0;
     bool ok = true;
+    // both parts' values of this row, combined by f (a bounded wait for the other warp)
+    auto exchange = [&](float mine, float& other) -> bool {
+      float* buf = row_max + (nx & 1) * 2 * kRows;
+      buf[part * kRows + r] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x_bar[quarter]);
+      if (!warp_wait(&x_bar[quarter], nx & 1, p.err, abort_flag)) return false;
+      ++nx;
+      other = buf[(1 - part) * kRows + r];
+      return true;
+    };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const Unit x = get_unit<kSrc>(p, u, nullptr);
       if (!x.rows) continue;
@@ -816,11 +768,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(s_full, gi & 1, p.err, abort_flag))) break;
         if (!(ok = warp_wait(&k_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;  // (long past: orders the masks)
         tc_fence_after();
-        uint32_t sv[64];
+        uint32_t sv[kCols];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_S + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
+        for (int c = 0; c < kCols / 16; ++c)
+          tmem_ld16(lane_base + TM_S + part * kCols + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
         uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + slot * 8);
-        const uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * 8);
+        uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * 8);
         const int d = limit - (x.lo + j * kTile);  // this row sees the tile's keys 0 .. d
         if (d < 63) valid &= d < 0 ? 0ull : (2ull << d) - 1ull;
         tmem_wait_ld();
@@ -828,8 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty);
         if (!__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
+          valid >>= part * kCols;
+          poison >>= part * kCols;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < kCols; ++c) {
             if ((poison >> c) & 1u) sv[c] = 0x7FC00000u;
             if (!((valid >> c) & 1u)) sv[c] = 0xFF800000u;
           }
@@ -838,38 +793,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(sv[c]);
 #pragma unroll
-        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        if (gi >= 1 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+        for (int c = 4; c < kCols; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if constexpr (kParts == 2) {
+          float other;
+          if (!(ok = exchange(mt, other))) break;
+          mt = fmaxf(mt, other);
+        }
         // Lazy rescale: a row's base m_used moves only when its maximum exceeds it by more than 2^8 (P stays
         // <= 256); the warp takes the step together, since the tensor-memory accesses are warp-collective.
-        if (__any_sync(0xFFFFFFFFu, mt > m_used + 8.0f)) {
+        const bool rescale = __any_sync(0xFFFFFFFFu, mt > m_used + 8.0f);
+        float f = 1.0f;
+        if (rescale) {
           const float m_new = mt > m_used + 8.0f ? mt : m_used;  // (a row's base depends on that row alone)
-          const float f = m_new == -INFINITY ? 1.0f : exp2f(m_used - m_new);  // 0 when m_used = -inf
-          if (j > 0) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int c0 = 0; c0 < kHalf; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-              tmem_ld16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-              tmem_st16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-              tmem_st16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-            }
-            tmem_wait_st();
-          }
+          f = m_new == -INFINITY ? 1.0f : exp2f(m_used - m_new);  // 0 when m_used = -inf
           l *= f;
           m_used = m_new;
         }
-        uint32_t pk[32];
+        uint32_t pk[kCols / 2];
         const float nsub = m_used == -INFINITY ? 0.0f : -m_used;
         float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), ns2 = make_float2(nsub, nsub);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
           const float2 e = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, ns2);
           const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
           // (the normaliser sums the weights before their rounding to bf16, which P V needs)
@@ -879,26 +825,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float2 pt = add2(ps[0], ps[1]);
         l += pt.x + pt.y;
-        uint8_t* prow = p_s + (r >> 3) * 1024 + (r & 7) * 16;
+        // O and the P buffer are free once the previous tile's P V has completed
+        if (gi >= 1 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+        if (rescale && j > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = part * (kHalf / kParts); c0 < (part + 1) * (kHalf / kParts); c0 += 32) {
+            uint32_t o[32];
+            tmem_ld16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_ld16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+            tmem_wait_ld();
 #pragma unroll
-        for (int kc = 0; kc < 8; ++kc)
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_st16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+          }
+          tmem_wait_st();
+        }
+        uint8_t* prow = p_s + (r >> 3) * 1024 + (r & 7) * 16 + part * (kCols / 8) * 128;
+#pragma unroll
+        for (int kc = 0; kc < kCols / 8; ++kc)
           *reinterpret_cast<uint4*>(prow + kc * 128) = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(p_full);
       }
       if (!ok) break;
+      if constexpr (kParts == 2) {
+        float other;
+        if (!(ok = exchange(l, other))) break;
+        l = part ? other + l : l + other;
+      }
       if (ntiles > 0 && !(ok = warp_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
       tc_fence_after();
       // a row that saw nothing: 0 and -inf; NaN stays NaN
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float lse = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
       if (u == last_u) {
-        stats[r] = inv;
+        if (part == 0) stats[r] = inv;
         mbar_arrive(ep_last);
       }
-      store_o(p, x, lane_base, quarter, 0, u == last_u ? 64 : kHalf, p_s + quarter * 4096, inv, ntiles > 0);
-      if (x.v == 0 && r < x.rows) {
+      const int lo = part * (kHalf / 2);
+      store_o(p, x, lane_base, quarter, lo, u == last_u ? lo + 64 : lo + kHalf / kParts, p_s + (warp - R::kSoftmaxWarp) * 2048, inv, ntiles > 0);
+      if (x.v == 0 && part == 0 && r < x.rows) {
         if (p.nsplit == 1) {
           if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;
         } else {
@@ -907,11 +876,151 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
+  } else {
+    if constexpr (kQuant)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssueRegs));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kIssueRegs));
+    if (warp == kIssueWarp) {
+      // ------------------------------------------------------------------ the products
+      // Order: Q K^T of tile g, then P V of tile g - 1.  So while the softmax reads S of tile g the tensor
+      // core works on P V, and it never idles for S's only buffer.
+      const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
+      const uint32_t idesc_o = idesc_f16(1u, 1u, (uint32_t)kRows, (uint32_t)kHalf);
+      const uint64_t qd = sw128_desc(smem_u32(q_s), 16, 1024);
+      const uint64_t pd = noswz_desc(smem_u32(p_s), 128, 1024);
+      const uint32_t d_s = tmem + TM_S, a_q = tmem + TM_Q, d_o = tmem + TM_O;
+      int gi = 0, ui = 0;
+      bool ok = true;
+      auto v_stage = [&](int g) { return smem_u32(smem + OFF_V + g % kVStages * kVBlocks * K_CHUNK); };
+      // P V of CTA tile g, the unit's first or a later one
+      auto issue_pv = [&](int g, bool first) -> bool {
+        if (!warp_wait(p_full, g & 1, p.err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t vd = sw128_desc(v_stage(g), K_CHUNK, 1024);
+        if (elect_one()) {
+          if (first)
+            umma_ss<0>(d_o, pd, vd, idesc_o);
+          else
+            umma_ss<1>(d_o, pd, vd, idesc_o);
+          umma_ss<1>(d_o, pd + 16, vd + 128, idesc_o);
+          umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
+          umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
+          mma_commit(pv_done);
+          mma_commit(&v_empty[g % kVStages]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit x = get_unit<kSrc>(p, u, nullptr);
+        if (!x.rows) continue;
+        const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+        if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
+        ++ui;
+        if (ntiles == 0) {
+          if (elect_one()) mma_commit(q_empty);
+          __syncwarp();
+        }
+        for (int j = 0; j < ntiles; ++j, ++gi) {
+          if (!(ok = warp_wait(&k_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
+          if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
+          tc_fence_after();
+          const uint64_t xd = sw128_desc(smem_u32(smem + OFF_X), 16, 1024);
+          const uint64_t yd = sw128_desc(smem_u32(smem + OFF_Y + gi % kYStages * kYBlocks * K_CHUNK), 16, 1024);
+          const uint64_t vd = sw128_desc(v_stage(gi), 16, 1024);
+          constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
+          if (elect_one()) {
+            // place c of the block order, 16 dims (32 bytes, 8 tensor-memory columns) per product; unrolled
+            // (a loop over the blocks issues a third more slowly)
+#pragma unroll
+            for (int i = 0; i < 4 * kChunks; ++i) {
+              const int c = i >> 2;
+              const uint64_t bd = (c < kXBlocks ? xd + (uint64_t)c * kc : c < kXBlocks + kYBlocks ? yd + (uint64_t)(c - kXBlocks) * kc
+                                                                       : vd + (uint64_t)(c - kXBlocks - kYBlocks) * kc) + (uint64_t)(i & 3) * 2;
+              if (i == 0)
+                umma_ss<0>(d_s, qd, bd, idesc_s);
+              else if (c < kSmemQ)
+                umma_ss<1>(d_s, qd + (uint64_t)c * qc + (uint64_t)(i & 3) * 2, bd, idesc_s);
+              else
+                umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), bd, idesc_s);
+              if (i == 4 * kXBlocks - 1) mma_commit(x_empty);
+              if (i == 4 * (kXBlocks + kYBlocks) - 1) mma_commit(&y_empty[gi % kYStages]);
+            }
+            mma_commit(s_full);
+            if (j == ntiles - 1) mma_commit(q_empty);
+          }
+          __syncwarp();
+          if (j > 0 && !(ok = issue_pv(gi - 1, j == 1))) break;
+        }
+        if (ok && ntiles > 0) ok = issue_pv(gi - 1, ntiles == 1);
+      }
+      if (elect_one()) mma_commit(fin);
+      __syncwarp();
+      mbar_wait(fin, 0, p.err, nullptr);
+    } else if (warp == R::kLookupWarp) {
+      // ------------------------------------------------------------------ pool rows of the keys, tiles ahead
+      int gi = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit x = get_unit<kSrc>(p, u, nullptr);
+        if (!x.rows) continue;
+        const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
+        const bool report = x.v == 0;
+        const int32_t* table = p.block_table + (int64_t)max(0, x.req) * p.max_blocks;
+        if constexpr (!kQuant) {
+          for (int j = 0; j < ntiles; ++j, ++gi) {
+            const int lblk = x.lo / kTile + j;
+            int page = lblk < p.max_blocks ? table[lblk] : -1;
+            if (page < 0 || page >= p.num_blocks) {
+              if (report) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+              page = -1;
+            }
+            if (gi >= kRowSlots && !(ok = warp_wait(&r_empty[gi % kRowSlots], ((gi / kRowSlots) - 1) & 1, p.err, abort_flag))) break;
+            if (lane == 0) {
+              row_ring[gi % kRowSlots] = page;
+              mbar_arrive(&r_full[gi % kRowSlots]);
+            }
+          }
+          continue;
+        }
+        // lane: keys lane and lane + 32 of a tile; the selected positions are loaded a tile ahead
+        auto position = [&](int j, int e) -> int {
+          const int slot = x.lo + j * kTile + lane + 32 * e;
+          if (slot >= x.hi) return -1;
+          return kSrc == kSelected && p.idx ? p.idx[(int64_t)(x.row0 / p.H) * p.k + slot] : slot;
+        };
+        int ps[2] = {position(0, 0), position(0, 1)};
+        for (int j = 0; j < ntiles; ++j, ++gi) {
+          const int next[2] = {position(j + 1, 0), position(j + 1, 1)};
+          int row[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            row[e] = -1;
+            const bool seen = x.req >= 0 && ps[e] >= 0 && (kSrc != kSelected || ps[e] <= x.tok0);
+            if (seen && ps[e] / kTile < p.max_blocks) row[e] = table[ps[e] / kTile];
+            if (seen && (row[e] < 0 || row[e] >= p.num_blocks)) {
+              if (report) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+              row[e] = -1;
+            }
+            if (row[e] >= 0) row[e] = row[e] * kTile + ps[e] % kTile;
+            if (kSrc == kSelected && !seen && ps[e] != -1 && x.req >= 0 && report) raise_error(p.err, DSA_DEVERR_INDEX);
+          }
+          if (gi >= kRowSlots && !(ok = warp_wait(&r_empty[gi % kRowSlots], ((gi / kRowSlots) - 1) & 1, p.err, abort_flag))) break;
+          row_ring[gi % kRowSlots * kTile + lane] = row[0];
+          row_ring[gi % kRowSlots * kTile + lane + 32] = row[1];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&r_full[gi % kRowSlots]);
+          ps[0] = next[0];
+          ps[1] = next[1];
+        }
+      }
+    }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kQkWarp) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, TM_COLS);
   }
@@ -1025,7 +1134,7 @@ cudaError_t launch(Params p, const MlaArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attrs[2];
-  const cudaLaunchConfig_t cfg = launch_config(dim3(units < num_sms ? units : num_sms), dim3(kThreads), SMEM, s, attrs);
+  const cudaLaunchConfig_t cfg = launch_config(dim3(units < num_sms ? units : num_sms), dim3(Roles<kSrc>::kThreads), SMEM, s, attrs);
   e = cudaLaunchKernelEx(&cfg, kernel, qmap, rmap, pmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   cudaLaunchAttribute cattrs[2];
