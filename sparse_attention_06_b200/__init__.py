@@ -130,9 +130,14 @@ def _check(status: int):
         raise DsaError(status, msg)
 
 
+# the current device and its current stream without the wrapper objects torch.cuda builds (~3 us a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -146,14 +151,15 @@ def _dev_ptr(t: Optional[torch.Tensor], what: str):
     return t.data_ptr()
 
 
+_DTYPE_CODES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16, torch.uint8: DSA_E4M3,
+                torch.float8_e4m3fn: DSA_E4M3}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return DSA_F32
-    if t.dtype == torch.bfloat16:
-        return DSA_BF16
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
-        return DSA_E4M3
-    raise ValueError("unsupported dtype %s" % t.dtype)
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    return code
 
 
 @dataclasses.dataclass
@@ -174,16 +180,16 @@ class PagedCache:
         return self.scale is not None and self.scale.dim() == 3
 
     def _c(self) -> _PagedCache:
-        nb, bs, dim = self.data.shape
-        if self._quantised_latent():
-            if _dtype_code(self.data) != DSA_E4M3 or dim != LATENT_E4M3_BYTES:
+        data, scale = self.data, self.scale
+        nb, bs, dim = data.shape
+        dtype = _dtype_code(data)
+        if scale is not None and scale.dim() == 3:
+            if dtype != DSA_E4M3 or dim != LATENT_E4M3_BYTES:
                 raise ValueError("a quantised latent cache has data [num_blocks, 64, 640] uint8")
-            if self.scale.dtype != torch.float32 or tuple(self.scale.shape) != (nb, bs, 4):
+            if scale.dtype != torch.float32 or scale.shape != (nb, bs, 4):
                 raise ValueError("a quantised latent cache has scale [num_blocks, 64, 4] float32")
-            return _PagedCache(_dev_ptr(self.data, "cache data"), _dev_ptr(self.scale, "cache scale"), nb, bs,
-                               LATENT_E4M3_DIM, DSA_LATENT_E4M3, 0)
-        return _PagedCache(_dev_ptr(self.data, "cache data"), _dev_ptr(self.scale, "cache scale"),
-                           nb, bs, dim, _dtype_code(self.data), 0)
+            dim, dtype = LATENT_E4M3_DIM, DSA_LATENT_E4M3
+        return _PagedCache(_dev_ptr(data, "cache data"), _dev_ptr(scale, "cache scale"), nb, bs, dim, dtype, 0)
 
 
 @dataclasses.dataclass
@@ -216,22 +222,24 @@ class Chunks:
     max_context: int
 
     def _c(self, num_tokens) -> _Chunks:
-        for n in ("cu_tokens", "seq_len", "block_table"):
-            if getattr(self, n).dtype != torch.int32:
-                raise ValueError("%s must be int32" % n)
-        B, mb = self.block_table.shape
-        if self.cu_tokens.shape != (B + 1,) or self.seq_len.shape != (B,):
+        cu, seq, table = self.cu_tokens, self.seq_len, self.block_table
+        i32 = torch.int32
+        if cu.dtype is not i32 or seq.dtype is not i32 or table.dtype is not i32:
+            raise ValueError("cu_tokens, seq_len and block_table must be int32")
+        B, mb = table.shape
+        if cu.shape != (B + 1,) or seq.shape != (B,):
             raise ValueError("cu_tokens must have B + 1 entries and seq_len B, for the B rows of block_table")
-        return _Chunks(int(num_tokens), B, _dev_ptr(self.cu_tokens, "cu_tokens"), _dev_ptr(self.seq_len, "seq_len"),
-                       _dev_ptr(self.block_table, "block_table"), mb, int(self.max_context))
+        return _Chunks(num_tokens, B, _dev_ptr(cu, "cu_tokens"), _dev_ptr(seq, "seq_len"),
+                       _dev_ptr(table, "block_table"), mb, int(self.max_context))
 
 
-def _same_device(*tensors):
-    """The library runs on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
+def _same_device(*tensors) -> int:
+    """The library runs on the current device: every tensor has to be there.  Returns the device."""
+    dev = _current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
+    return dev
 
 
 def dsa_indexer_scores(q, w, keys: PagedCache, batch: Batch, scores, stream=None, q_scale=None, key_hist=None):
@@ -324,9 +332,12 @@ def _rows(x, dim, what):
         raise ValueError("%s must be [num_tokens, %d]" % (what, dim))
     if not x.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    if x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < dim):
+    row, one = x.stride()
+    if x.shape[0] == 1:
+        row = dim
+    if one != 1 or row < dim:
         raise ValueError("%s: the elements of a row must be contiguous, and rows must not overlap" % what)
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else dim
+    return x.data_ptr(), row
 
 
 def dsa_cache_append(k, kv, keys: Optional[PagedCache], latent: Optional[PagedCache], chunks: Chunks, stream=None):
@@ -337,21 +348,28 @@ def dsa_cache_append(k, kv, keys: Optional[PagedCache], latent: Optional[PagedCa
     lib = load_library()
     if (k is None) != (keys is None) or (kv is None) != (latent is None):
         raise ValueError("k comes with keys, and kv with latent")
-    given = [x for x in (k, kv) if x is not None]
-    if not given:
+    x = k if k is not None else kv
+    if x is None:
         raise ValueError("nothing to append")
-    if len(given) == 2 and (k.shape[0] != kv.shape[0] or k.dtype != kv.dtype):
-        raise ValueError("k and kv must have the same tokens and dtype")
-    kc = keys._c() if keys is not None else None
-    lc = latent._c() if latent is not None else None
-    cc = chunks._c(given[0].shape[0])
-    _same_device(k, kv, chunks.cu_tokens, *(c.data for c in (keys, latent) if c is not None))
-    kp, ks = _rows(k, kc.dim, "k") if kc is not None else (None, 0)
-    vp, vs = _rows(kv, lc.dim, "kv") if lc is not None else (None, 0)
-    if given[0].shape[0] == 0:
+    T = x.shape[0]
+    kp = vp = kc = lc = None
+    ks = vs = 0
+    if keys is not None:
+        kc = keys._c()
+        kp, ks = _rows(k, kc.dim, "k")
+    if latent is not None:
+        lc = latent._c()
+        vp, vs = _rows(kv, lc.dim, "kv")
+        if kv.shape[0] != T or kv.dtype is not x.dtype:
+            raise ValueError("k and kv must have the same tokens and dtype")
+    cc = chunks._c(T)
+    dev = _same_device(k, kv, chunks.cu_tokens, keys.data if keys is not None else None,
+                       latent.data if latent is not None else None)
+    if T == 0:
         return
-    _check(lib.dsa_cache_append(kp, ks, vp, vs, _dtype_code(given[0]), ctypes.byref(kc) if kc is not None else None,
-                                ctypes.byref(lc) if lc is not None else None, ctypes.byref(cc), _stream(stream)))
+    status = lib.dsa_cache_append(kp, ks, vp, vs, _dtype_code(x), kc, lc, cc, _raw_stream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(status)
 
 
 def dsa_cache_read(cache: PagedCache, chunks: Chunks, out, stream=None):
@@ -361,11 +379,14 @@ def dsa_cache_read(cache: PagedCache, chunks: Chunks, out, stream=None):
     c = cache._c()
     if out.dim() != 2 or out.shape[1] != c.dim:
         raise ValueError("out must be [num_tokens, %d]" % c.dim)
-    cc = chunks._c(out.shape[0])
-    _same_device(cache.data, out, chunks.cu_tokens)
-    if out.shape[0]:
-        _check(lib.dsa_cache_read(ctypes.byref(c), ctypes.byref(cc), _dev_ptr(out, "out"), _dtype_code(out),
-                                  _stream(stream)))
+    T = out.shape[0]
+    cc = chunks._c(T)
+    dev = _same_device(cache.data, out, chunks.cu_tokens)
+    if T:
+        status = lib.dsa_cache_read(c, cc, _dev_ptr(out, "out"), _dtype_code(out),
+                                    _raw_stream(dev) if stream is None else _stream(stream))
+        if status:
+            _check(status)
     return out
 
 
@@ -376,17 +397,19 @@ def dsa_chunk_mla(q, latent: PagedCache, chunks: Chunks, softmax_scale, out, lse
     lib = load_library()
     T, H, dqk = q.shape
     d_v = out.shape[-1]
-    if tuple(out.shape) != (T, H, d_v) or out.dtype != q.dtype:
+    if out.shape != (T, H, d_v) or out.dtype is not q.dtype:
         raise ValueError("out must be [num_tokens, H, d_v] of q's dtype")
-    if lse is not None and (tuple(lse.shape) != (T, H) or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != (T, H) or lse.dtype is not torch.float32):
         raise ValueError("lse must be [num_tokens, H] float32")
     lc, cc = latent._c(), chunks._c(T)
-    _same_device(q, latent.data, out, lse, workspace, chunks.cu_tokens)
+    dev = _same_device(q, latent.data, out, lse, workspace, chunks.cu_tokens)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if T:
-        _check(lib.dsa_chunk_mla(_dev_ptr(q, "q"), _dtype_code(q), H, d_v, dqk - d_v, ctypes.byref(lc),
-                                 ctypes.byref(cc), float(softmax_scale), _dev_ptr(out, "out"), _dev_ptr(lse, "lse"),
-                                 _dev_ptr(workspace, "workspace"), ws_bytes, _stream(stream)))
+        status = lib.dsa_chunk_mla(_dev_ptr(q, "q"), _dtype_code(q), H, d_v, dqk - d_v, lc, cc, float(softmax_scale),
+                                   _dev_ptr(out, "out"), _dev_ptr(lse, "lse"), _dev_ptr(workspace, "workspace"), ws_bytes,
+                                   _raw_stream(dev) if stream is None else _stream(stream))
+        if status:
+            _check(status)
     return out
 
 
