@@ -503,12 +503,12 @@ dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v,
   // queries or outputs off a 16-byte boundary cannot be copied as tiles
   if (!chunk_tensor_cores(q_dtype, H, d_v, d_rope) || !aligned16(q) || !aligned16(out))
     return cuda_status(launch_chunk_mla_generic(a, *chunks, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch", 1);
-  const int nsplit = chunk_mla_splits(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, sms);
-  const size_t need = chunk_mla_workspace(chunks->num_tokens, chunks->num_reqs, H, nsplit);
+  const int split = chunk_mla_split_tiles(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, sms);
+  const size_t need = chunk_mla_workspace(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, split);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(DSA_ERR_INVALID_ARG, "chunk mla: workspace missing, too small or not 256-byte aligned%s");
-  return cuda_status(launch_chunk_mla_tc(a, *chunks, nsplit, sms, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch",
-                     nsplit > 1 ? 2 : 1);
+  return cuda_status(launch_chunk_mla_tc(a, *chunks, split, sms, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch",
+                     need > 0 ? 2 : 1);
 }
 
 size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
@@ -516,7 +516,8 @@ size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_
   if (num_tokens < 1 || num_reqs < 1 || max_context < 1 || !chunk_tensor_cores(DSA_BF16, H, d_v, 64)) return 0;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return chunk_mla_workspace(num_tokens, num_reqs, H, chunk_mla_splits(num_tokens, num_reqs, H, max_context, sms));
+  return chunk_mla_workspace(num_tokens, num_reqs, H, max_context,
+                             chunk_mla_split_tiles(num_tokens, num_reqs, H, max_context, sms));
 }
 
 dsa_status dsa_selftest_bounded_wait(int64_t limit_cycles, dsa_stream stream) {

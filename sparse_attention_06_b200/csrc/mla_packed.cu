@@ -48,8 +48,7 @@ constexpr int kRows = 128;               // query rows per tile (MMA M)
 constexpr int kTile = 64;                // keys per tile = tokens per page
 constexpr int kChunks = 9;               // 64-dim column blocks of a row
 constexpr int kSmemQ = 3;                // Q blocks in shared memory (the first that Q K^T uses), the rest in tensor memory
-constexpr int kFillWarps = 8;
-constexpr int kKeysPerWarp = kTile / kFillWarps;  // 8
+constexpr int kFillWarps = 8, kKeysPerWarp = kTile / kFillWarps;
 constexpr int kLatentBytes = 640;        // data bytes of a quantised row
 
 // A tile's blocks in the order Q K^T uses them: X0 (RoPE), X1, Y0, Y1, Y2 (the values of the other
@@ -69,14 +68,16 @@ constexpr int OFF_Y = OFF_P + kRows * kTile * 2;
 constexpr int OFF_X = OFF_Y + kYStages * kYBlocks * K_CHUNK;
 constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;
 constexpr int OFF_BAR = OFF_V + kVStages * kVBlocks * K_CHUNK;
-constexpr int NBAR = 32;
+constexpr int NBAR = 36;
 constexpr int kMaskSlots = 4;
-constexpr int OFF_MASK = OFF_BAR + NBAR * 8;             // [slot] 64-bit mask of real rows (a byte per warp)
-constexpr int OFF_POISON = OFF_MASK + kMaskSlots * 8;    // [slot] rows with NaN or infinity, see below
+constexpr int kMaskBytes = 8;                            // of a slot: one byte per fill warp, a bit per key
+constexpr int OFF_MASK = OFF_BAR + NBAR * 8;             // [slot] keys with a row to see
+constexpr int OFF_POISON = OFF_MASK + kMaskSlots * kMaskBytes;  // [slot] rows with NaN or infinity, see below
 constexpr int kRowSlots = 4;
-constexpr int OFF_STATS = OFF_POISON + kMaskSlots * 8;   // 1 / l of each row (last unit)
+constexpr int OFF_STATS = OFF_POISON + kMaskSlots * kMaskBytes;   // 1 / l of each row (last unit)
 constexpr int OFF_MISC = OFF_STATS + kRows * 4;
-constexpr int OFF_ROWS = OFF_MISC + 32;                  // quantised: [slot][64] pool row of each key of a tile, -1: none to see;
+constexpr int OFF_UNIT = OFF_MISC + 16;                  // [2] units in hand
+constexpr int OFF_ROWS = OFF_UNIT + 2 * 40;                  // quantised: [slot][64] pool row of each key of a tile, -1: none to see;
                                                          // bf16: [slot] page of the tile, then [2][2][128] row maxima exchanged
 constexpr int SMEM = OFF_ROWS + kRowSlots * 4 + 2 * 2 * kRows * 4;
 static_assert(kRowSlots * kTile * 4 <= 2 * 2 * kRows * 4, "row ring");
@@ -107,8 +108,11 @@ struct Roles {
   static constexpr int kFillRegs = kQuant ? 136 : 80, kSoftmaxRegs = kQuant ? 136 : 104, kIssueRegs = 104;
 };
 
+constexpr int kUnitSlots = 2;
+
 struct Params {
   const uint8_t* data;    // pool rows
+  const __nv_bfloat16* q;  // [T, H, 576]
   const float* scale;     // quantised: [pool rows, 4]
   const int32_t* idx;     // kSelected: [T, k] or null (every visible position)
   const int32_t *q_req, *q_pos;
@@ -118,21 +122,24 @@ struct Params {
   float* lse;             // [T, H] or null
   float *part_o, *part_lse;  // several splits: [tiles, nsplit, prows, 512] and [tiles, nsplit, prows]
   int32_t num_blocks, oob_row;
-  int T, H, k, ks, nsplit, prows, tiles, num_reqs, max_blocks, max_context;
+  int T, H, k, ks, nsplit, per, prows, tiles, num_reqs, max_blocks, max_context;
+  int* next;              // units handed out beyond the first of each CTA (zero at launch), or null: round robin
   float scale_log2;       // softmax scale * log2(e)
   int* err;
 };
 
-// A unit of work (rows 0 of an unused one: nothing to do).
+// A unit of work.
 struct Unit {
-  int rows;       // query rows in use
+  int rows;       // query rows in use; 0: nothing to do, -1: no more units
   int row0;       // first of them in the [T * H] query rows
   int req;        // request (-1: the query is invalid, it sees nothing)
   int tok0, h0;   // kPages*: token of row 0 within its chunk's positions (its position), its head
   int lo, hi;     // keys: selection slots or positions [lo, hi)
+  int splits;     // of the row tile: 1 writes the output, more write partials
   int prow;       // first partial row
   int v;
 };
+static_assert(sizeof(Unit) == 40, "unit ring");
 
 template <bool B>
 struct Flag {
@@ -188,6 +195,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Tiles of a batch of chunks: request r has the tile numbers first_tile(r) .. first_tile(r + 1) - 1, at
 // least as many as its rows need (ceil(b - a) <= floor(b) - floor(a) + 1); the rest are unused.  So a
 // tile's request follows from cu_tokens alone, by a search instead of a prefix sum.
@@ -211,12 +228,14 @@ __device__ __forceinline__ int tile_request(const dsa_chunks& c, int H, int tile
   }
 }
 
-// Keys of split sp of a row tile that sees positions 0 .. len - 1: whole key tiles, evenly.
-__device__ __forceinline__ void split_range(int len, int nsplit, int sp, int& lo, int& hi) {
-  const int tiles = (len + kTile - 1) / kTile;
-  const int per = (tiles + nsplit - 1) / nsplit;
-  lo = min(len, sp * per * kTile);
-  hi = min(len, lo + per * kTile);
+// Key splits of a row tile that sees positions 0 .. len - 1: as many as it takes for at most `per` key tiles each
+// (units of like size keep the CTAs busy to the end, however ragged the batch), and split sp's keys: whole
+// key tiles, evenly.
+__device__ __forceinline__ int split_count(int len, int per) { return ((len + kTile - 1) / kTile + per - 1) / per; }
+__device__ __forceinline__ void split_range(int len, int splits, int sp, int& lo, int& hi) {
+  const int tiles = (len + kTile - 1) / kTile, each = (tiles + splits - 1) / splits;
+  lo = min(len, sp * each * kTile);
+  hi = min(len, lo + each * kTile);
 }
 
 // Row tile `i` of request r: its rows, the position of its first and behind its last token.
@@ -245,6 +264,7 @@ __device__ __forceinline__ Unit get_unit(const Params& p, int u, int* err) {
   Unit x;
   x.rows = 0;
   x.v = u & 1;
+  x.splits = p.nsplit;
   const int ts = u >> 1;
   const int sp = ts % p.nsplit;
   int tile = ts / p.nsplit;
@@ -272,26 +292,40 @@ __device__ __forceinline__ Unit get_unit(const Params& p, int u, int* err) {
       return x;
     }
     x.req = r;
-    split_range(len, p.nsplit, sp, x.lo, x.hi);
-    if (x.lo >= x.hi) x.rows = 0;  // (a split without keys leaves no partial: the combine knows it)
+    x.splits = split_count(len, p.per);
+    split_range(len, x.splits, sp, x.lo, x.hi);
+    if (sp >= x.splits || x.lo >= x.hi) x.rows = 0;  // (a split without keys leaves no partial: the combine knows it)
   }
   x.prow = (tile * p.nsplit + sp) * p.prows;
   return x;
 }
 
-// Codes times a power of two, as four bf16 pairs: the code's exponent and mantissa
-// are moved to a bf16's, whose value is then the code's times 2^-120 (subnormal codes become
-// subnormal bf16), and one exact product by 2^(e + 120) does the rest; `m2` (1 unless e > 7, where 2^(e + 120) is
-// no bf16) takes what is left.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// The unit after u of a CTA (warp-collective): round robin, or, where units differ in size, the next one nobody has.
+__device__ __forceinline__ int next_unit(const Params& p, int u) {
+  if (!p.next) return u + (int)gridDim.x;
+  int n = 0;
+  if ((threadIdx.x & 31) == 0) n = (int)gridDim.x + atomicAdd(p.next, 1);
+  return __shfl_sync(0xFFFFFFFFu, n, 0);
 }
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t m, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-  lo = mul_bf16x2(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), m);
-  hi = mul_bf16x2(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), m);
+
+// Four codes times their scale as two bf16 pairs, all exact (four significant bits and a power of two): the
+// hardware's e4m3 -> f16 conversion, f32 products, one packing conversion.  Of the ten instructions four are ALU ones;
+// moving the code's bits into a bf16's with integer operations took thirteen, eleven of them ALU, whose
+// half-rate pipe then bounds the kernel.
+__device__ __forceinline__ void decode4(uint32_t w, float2 s, uint32_t& lo, uint32_t& hi) {
+  uint32_t h[2], b[2];
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h[i])), s);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
+    b[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  lo = b[0];
+  hi = b[1];
 }
 
 // O_v / l of this warp's 32 rows, columns [c_lo, c_hi) (multiples of 32), from tensor memory to the
@@ -300,7 +334,7 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t m, uint32_t& lo, ui
 __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t lane_base, int quarter, int c_lo, int c_hi,
                                         uint8_t* stage, float inv, bool have_o) {
   const int lane = threadIdx.x & 31;
-  const bool f32out = p.nsplit > 1;
+  const bool f32out = x.splits > 1;
   const int rows = min(32, x.rows - quarter * 32);
   uint8_t* mine = stage + lane * 64;
   const int mix = (lane >> 1) & 3;
@@ -395,6 +429,9 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
   uint8_t* masks = smem + OFF_MASK;
   int32_t* row_ring = reinterpret_cast<int32_t*>(smem + OFF_ROWS);
   float* row_max = reinterpret_cast<float*>(smem + OFF_ROWS + kRowSlots * 4);
+  uint64_t* u_full = bars + 32;     // [kUnitSlots] a unit (or the end) published
+  uint64_t* u_empty = bars + 34;    // [kUnitSlots] ... taken by every warp that works on it
+  Unit* unit_ring = reinterpret_cast<Unit*>(smem + OFF_UNIT);
   uint64_t* x_bar = bars + 28;      // [4] the two softmax warps of 32 rows have exchanged their maxima
   uint8_t* poisons = smem + OFF_POISON;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -419,15 +456,19 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
     for (int i = 0; i < kVStages; ++i) mbar_init(&v_empty[i], 1);
     mbar_init(q_stage, 1);
     mbar_init(q_read, kFillWarps);
-    mbar_init(q_full, 32 * kFillWarps);
+    mbar_init(q_full, kFillWarps);
     mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(s_empty, 4 * kParts);
-    mbar_init(p_full, 128 * kParts);
+    mbar_init(p_full, 4 * kParts);
     mbar_init(pv_done, 1);
     mbar_init(fin, 1);
     mbar_init(ep_last, 128 * kParts);
     for (int i = 0; i < 4; ++i) mbar_init(&x_bar[i], 2);
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], kIssueWarp + 1);  // fill, softmax, issue
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -441,15 +482,20 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
 
-  // the CTA's last unit that has work (its epilogue is shared among the warps)
-  int last_u = -1;
-  if (warp < kIssueWarp) {
-    for (int u = blockIdx.x + (units - 1 - (int)blockIdx.x) / (int)gridDim.x * (int)gridDim.x; u >= 0; u -= gridDim.x)
-      if (get_unit<kSrc>(p, u, nullptr).rows) {
-        last_u = u;
-        break;
-      }
-  }
+  // unit number k of this CTA (the lookup warp publishes it; false: none, or gave up)
+  auto take_unit = [&](int k, Unit& x) -> bool {
+    if (!warp_wait(&u_full[k % kUnitSlots], (k / kUnitSlots) & 1, p.err, abort_flag)) return false;
+    x = unit_ring[k % kUnitSlots];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[k % kUnitSlots]);
+    return x.rows > 0;
+  };
+  // whether unit k is the CTA's last (asked when its work is done, so that the next is known)
+  auto last_unit = [&](int k, bool& last) -> bool {
+    if (!warp_wait(&u_full[(k + 1) % kUnitSlots], ((k + 1) / kUnitSlots) & 1, p.err, abort_flag)) return false;
+    last = unit_ring[(k + 1) % kUnitSlots].rows < 0;
+    return true;
+  };
 
   if (warp < kFillWarps) {
     if constexpr (kQuant)
@@ -463,36 +509,35 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
     int gi = 0, ui = 0;
     uint32_t nland[2] = {0u, 0u};
     bool ok = true, staged = false;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit x = get_unit<kSrc>(p, u, tid == 0 && (u & 1) == 0 ? p.err : nullptr);
-      if (!x.rows) continue;
+    Unit x;
+    for (; ok && take_unit(ui, x);) {
       const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
       const bool report = x.v == 0;
 
-      // pool row of key `key` of this warp's eight, of CTA tile g (r_full of that tile has been waited for)
+      // pool row of key `key` of this warp's, of CTA tile g (r_full of that tile has been waited for)
       auto row_of = [&](int g, int key) -> int { return row_ring[g % kRowSlots * kTile + warp * kKeysPerWarp + key]; };
       auto wait_rows = [&](int g) { return warp_wait(&r_full[g % kRowSlots], (g / kRowSlots) & 1, p.err, abort_flag); };
 
-      // --- quantised rows in flight: pair q is the rows 8 warp + 2 q + half; a lane has 16 of its codes in
-      // this CTA's value half (hh = 0) and 16 in the other (hh = 1).  Lane l has the scale of row l / 4, group
-      // l % 4, of the warp's eight rows.  Loads of one kind are issued together, as far as possible ahead of
+      // --- quantised rows in flight: pair q is the warp's keys 2 q + half; a lane has 16 codes of its row in
+      // this CTA's value half (hh = 0) and 16 in the other (hh = 1).  Lane l has the scale of key l / 4 % 4, group
+      // l % 4.  Loads of one kind are issued together, as far as possible ahead of
       // their use: a warp waits for loads by a handful of counters, so waiting for an old load can mean waiting
       // for a young one that shares its counter.  None is conditional (a key without a row reads row 0).
-      uint4 code[4][2];
+      constexpr int kPairs = kKeysPerWarp / 2;
+      constexpr uint32_t kAll = (1u << kKeysPerWarp) - 1u;
+      uint4 code[kPairs][2];
       float sc = 1.0f;
       uint32_t seen = 0u, bad = 0u;  // of the tile in registers: keys with a row; lanes with no row or no power of two
-      bool all_plain = true;
       auto load_codes = [&](int g, int hh) {
         const uint8_t* base = p.data + 256 * (hh ^ x.v) + 16 * l16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) code[q][hh] = load16_here(base + (int64_t)max(0, row_of(g, 2 * q + half)) * kLatentBytes);
+        for (int q = 0; q < kPairs; ++q) code[q][hh] = load16_here(base + (int64_t)max(0, row_of(g, 2 * q + half)) * kLatentBytes);
       };
-      auto load_scales = [&](int g) -> float { return loadf_here(p.scale + (int64_t)max(0, row_of(g, lane >> 2)) * 4 + (lane & 3)); };
+      auto load_scales = [&](int g) -> float { return loadf_here(p.scale + (int64_t)max(0, row_of(g, (lane >> 2) & (kKeysPerWarp - 1))) * 4 + (lane & 3)); };
       auto check_rows = [&](int g) {
-        const bool none = row_of(g, lane >> 2) < 0;
+        const bool none = row_of(g, (lane >> 2) & (kKeysPerWarp - 1)) < 0;
         bad = __ballot_sync(0xFFFFFFFFu, none || !latent_scale_ok(sc));
         seen = ~__ballot_sync(0xFFFFFFFFu, none);
-        all_plain = bad == 0u && !__any_sync(0xFFFFFFFFu, sc > 128.0f);
       };
       if (kQuant && ntiles > 0) {
         if (!(ok = wait_rows(gi))) break;
@@ -536,9 +581,11 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(q_full);
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_read);
+      if (lane == 0) {
+        mbar_arrive(q_full);
+        mbar_arrive(q_read);
+      }
       if (!(ok = warp_wait(q_read, ui & 1, p.err, abort_flag))) break;
       ++ui;
 
@@ -552,45 +599,48 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
         auto wait_y = [&]() { return gi < kYStages || warp_wait(&y_empty[gi % kYStages], ((gi / kYStages) - 1) & 1, p.err, abort_flag); };
         auto wait_x = [&]() { return gi < 1 || warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag); };
         if constexpr (kQuant) {
-          uint32_t nan[4] = {0u, 0u, 0u, 0u};
+          // rows that only some of the tile's tokens see: a NaN there must not reach the others through 0 * NaN
+          // in P V, so it becomes zero and its row is noted: the softmax makes the weights of the tokens that see
+          // it NaN (elsewhere a NaN takes its natural course)
+          const bool partly = kSrc != kSelected && x.lo + j * kTile + kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
+          uint32_t nan_rows = 0u;
           // 16 codes into the row's blocks: `dst` is the row of the lane's 64-dim block, pieces 2 (l16 % 4) and
           // the next; eight consecutive lanes hold four pieces of both rows of a pair, which differ in bit 0, so
-          // they store to all eight bank groups.  kPlain: every key has a row, and scales are at most 2^7.
+          // they store to all eight bank groups.  kPlain: every key has a row, and all tokens see them.
           auto put = [&](auto plain, int q, int hh, uint8_t* dst) {
             constexpr bool kPlain = decltype(plain)::value;
             const int r = warp * kKeysPerWarp + 2 * q + half;
             uint32_t w[4] = {code[q][hh].x, code[q][hh].y, code[q][hh].z, code[q][hh].w};
-            const float my_sc = __shfl_sync(0xFFFFFFFFu, sc, (2 * q + half) * 4 + 2 * (hh ^ x.v) + (l16 >> 3));
-            // 2^(e - 127 + 120) as a bf16 pair (e: the scale's biased exponent), at most 2^127; m2: the rest
-            const uint32_t e = __float_as_uint(my_sc) >> 23, e1 = kPlain ? e + 120u : min(e + 120u, 254u);
-            const uint32_t m1 = e1 * 0x00800080u;
-            if (!kPlain && ((bad >> (4 * (2 * q + half))) & 0xFu)) w[0] = w[1] = w[2] = w[3] = 0u;
+            float my_sc = __shfl_sync(0xFFFFFFFFu, sc, (2 * q + half) * 4 + 2 * (hh ^ x.v) + (l16 >> 3));
+            if (!kPlain && ((bad >> (4 * (2 * q + half))) & 0xFu)) {
+              w[0] = w[1] = w[2] = w[3] = 0u;
+              my_sc = 1.0f;
+            }
             uint32_t b[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              nan[q] |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: that code is NaN
-              decode4(w[i], m1, b[2 * i], b[2 * i + 1]);
-            }
-            if (!kPlain && e > 134u) {
-              const uint32_t m2 = (min(e, 246u) - 134u + 127u) * 0x00800080u;
+            for (int i = 0; i < 4; ++i) decode4(w[i], make_float2(my_sc, my_sc), b[2 * i], b[2 * i + 1]);
+            if (!kPlain && partly) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(b[i], m2);
+              for (int i = 0; i < 8; ++i) {
+                if ((b[i] & 0x7F80u) == 0x7F80u) { b[i] &= 0xFFFF0000u; nan_rows |= 1u << (2 * q + half); }
+                if ((b[i] & 0x7F800000u) == 0x7F800000u) { b[i] &= 0xFFFFu; nan_rows |= 1u << (2 * q + half); }
+              }
             }
             const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
             *reinterpret_cast<uint4*>(dst + r * 128 + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
             *reinterpret_cast<uint4*>(dst + r * 128 + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
           };
-          auto put4 = [&](int hh, uint8_t* dst) {
-            if (all_plain) {
+          auto put_all = [&](int hh, uint8_t* dst) {
+            if (bad == 0u && !partly) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) put(Flag<true>(), q, hh, dst);
+              for (int q = 0; q < kPairs; ++q) put(Flag<true>(), q, hh, dst);
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) put(Flag<false>(), q, hh, dst);
+              for (int q = 0; q < kPairs; ++q) put(Flag<false>(), q, hh, dst);
             }
           };
           if (!(ok = wait_v())) break;
-          put4(0, v_st + (l16 >> 2) * K_CHUNK);
+          put_all(0, v_st + (l16 >> 2) * K_CHUNK);
           const bool more = j + 1 < ntiles;
           float sc_n = 1.0f;
           if (more) {
@@ -601,7 +651,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           if (!(ok = wait_y()) || !(ok = wait_x())) break;
           // the RoPE part as it is, in the background (zeros for a row that is not there)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < kKeysPerWarp / 4; ++i) {
             const int r8 = 4 * i + (lane >> 3);
             const int r = warp * kKeysPerWarp + r8;
             cp_async_16(smem_u32(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
@@ -610,13 +660,10 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&r_empty[gi % kRowSlots]);
-          put4(1, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK);
-          uint32_t nan_rows = 0u;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) nan_rows |= (nan[q] & 0x80808080u) ? 1u << (2 * q + half) : 0u;
+          put_all(1, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK);
           const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
           if (lane == 0) {
-            uint32_t valid = 0xFFu;
+            uint32_t valid = kAll;
             if (bad) {
               bool flag = false;
               for (int r8 = 0; r8 < kKeysPerWarp; ++r8)
@@ -626,8 +673,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
                 }
               if (report && flag) raise_error(p.err, DSA_DEVERR_SCALE);
             }
-            masks[slot * 8 + warp] = (uint8_t)valid;
-            poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
+            masks[slot * kMaskBytes + warp] = (uint8_t)valid;
+            poisons[slot * kMaskBytes + warp] = (uint8_t)(poison & valid);
           }
           if (more) {
             sc = sc_n;
@@ -646,8 +693,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           if (lane == 0) mbar_arrive(&r_empty[gi % kRowSlots]);
           const int base = x.lo + j * kTile;
           const bool whole = base + kTile <= x.hi && valid == 0xFFu;
-          // rows that only some of the tile's tokens see: a NaN there must not reach the others through
-          // 0 * NaN in P V.  They are looked over once they have landed, see below.
+          // (as above; these rows are looked over once they have landed)
           const bool partly = base + kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
           uint64_t* bar = partly ? &land[s] : &k_full[s];
           // this warp's eight rows (or, for a whole page, warp 0 all of them): places lo .. hi - 1 of the order
@@ -669,8 +715,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           };
           if (!(ok = wait_y())) break;
           if (lane == 0) {
-            masks[slot * 8 + warp] = (uint8_t)valid;
-            if (!partly) poisons[slot * 8 + warp] = 0;
+            masks[slot * kMaskBytes + warp] = (uint8_t)valid;
+            if (!partly) poisons[slot * kMaskBytes + warp] = 0;
             fence_proxy_async_smem();
             if (!whole)
               mbar_arrive_expect_tx(bar, kKeysPerWarp * kDqk * 2);
@@ -708,7 +754,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
               if (f) *at = make_uint4(w[0], w[1], w[2], w[3]);
               if (__any_sync(0xFFFFFFFFu, f)) poison |= 1u << r8;
             }
-            if (lane == 0) poisons[slot * 8 + warp] = (uint8_t)poison;
+            if (lane == 0) poisons[slot * kMaskBytes + warp] = (uint8_t)poison;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_full[s]);
@@ -716,12 +762,16 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
         }
       }
       if (!ok) break;
-      if (u == last_u) {
+      bool last;
+      if (!(ok = last_unit(ui - 1, last))) break;
+      if (last) {
         // the CTA's last unit: these warps store part of O_v / l too, staged in the V ring (free after the last P V)
         if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
         tc_fence_after();
-        const int lo = kParts == 2 ? 64 + 128 * part : 64 + 96 * part;
-        store_o(p, x, my_lanes, quarter, lo, lo + (kParts == 2 ? 64 : 96), smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], ntiles > 0);
+        // (of the 256 columns 64 are each softmax warp's)
+        const int width = kParts == 2 ? 64 : 96, lo = 64 + (kParts == 2 ? 128 : 96) * part;
+        store_o(p, x, my_lanes, quarter, lo, lo + width, smem + OFF_V + warp * 2048,
+                stats[quarter * 32 + lane], ntiles > 0);
         tc_fence_before();
       }
     }
@@ -752,9 +802,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
       other = buf[(1 - part) * kRows + r];
       return true;
     };
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit x = get_unit<kSrc>(p, u, nullptr);
-      if (!x.rows) continue;
+    Unit x;
+    for (int ui = 0; ok && take_unit(ui, x); ++ui) {
       const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
       // last position this row sees (kSelected: the tile's own mask tells)
       int limit;
@@ -772,8 +821,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kCols / 16; ++c)
           tmem_ld16(lane_base + TM_S + part * kCols + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
-        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + slot * 8);
-        uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * 8);
+        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + slot * kMaskBytes);
+        uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * kMaskBytes);
         const int d = limit - (x.lo + j * kTile);  // this row sees the tile's keys 0 .. d
         if (d < 63) valid &= d < 0 ? 0ull : (2ull << d) - 1ull;
         tmem_wait_ld();
@@ -848,7 +897,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           *reinterpret_cast<uint4*>(prow + kc * 128) = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
       if constexpr (kParts == 2) {
@@ -861,14 +911,16 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
       // a row that saw nothing: 0 and -inf; NaN stays NaN
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float lse = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
-      if (u == last_u) {
+      bool last;
+      if (!(ok = last_unit(ui, last))) break;
+      if (last) {
         if (part == 0) stats[r] = inv;
         mbar_arrive(ep_last);
       }
       const int lo = part * (kHalf / 2);
-      store_o(p, x, lane_base, quarter, lo, u == last_u ? lo + 64 : lo + kHalf / kParts, p_s + (warp - R::kSoftmaxWarp) * 2048, inv, ntiles > 0);
+      store_o(p, x, lane_base, quarter, lo, last ? lo + 64 : lo + kHalf / kParts, p_s + (warp - R::kSoftmaxWarp) * 2048, inv, ntiles > 0);
       if (x.v == 0 && part == 0 && r < x.rows) {
-        if (p.nsplit == 1) {
+        if (x.splits == 1) {
           if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;
         } else {
           p.part_lse[(int64_t)x.prow + r] = lse;
@@ -912,9 +964,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
         __syncwarp();
         return true;
       };
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit x = get_unit<kSrc>(p, u, nullptr);
-        if (!x.rows) continue;
+      Unit x;
+      for (; ok && take_unit(ui, x);) {
         const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
         if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
         ++ui;
@@ -962,9 +1013,23 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
       // ------------------------------------------------------------------ pool rows of the keys, tiles ahead
       int gi = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit x = get_unit<kSrc>(p, u, nullptr);
-        if (!x.rows) continue;
+      int u = blockIdx.x;
+      for (int k = 0; ok; ++k) {
+        Unit x;
+        x.rows = -1;
+        for (; u < units;) {
+          x = get_unit<kSrc>(p, u, lane == 0 && (u & 1) == 0 ? p.err : nullptr);
+          if (x.rows > 0) break;
+          u = next_unit(p, u);
+          x.rows = -1;
+        }
+        if (k >= kUnitSlots && !(ok = warp_wait(&u_empty[k % kUnitSlots], ((k / kUnitSlots) - 1) & 1, p.err, abort_flag))) break;
+        if (lane == 0) {
+          unit_ring[k % kUnitSlots] = x;
+          mbar_arrive(&u_full[k % kUnitSlots]);
+        }
+        if (x.rows < 0) break;
+        u = next_unit(p, u);
         const int ntiles = (x.hi - x.lo + kTile - 1) / kTile;
         const bool report = x.v == 0;
         const int32_t* table = p.block_table + (int64_t)max(0, x.req) * p.max_blocks;
@@ -982,6 +1047,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
               mbar_arrive(&r_full[gi % kRowSlots]);
             }
           }
+          if (!ok) break;
           continue;
         }
         // lane: keys lane and lane + 32 of a tile; the selected positions are loaded a tile ahead
@@ -1046,8 +1112,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
     tile = (int)first_tile(p.chunks.cu_tokens[req], req, p.H) + i;
     int rows, row0, tok0, h0, len;
     if (!chunk_tile(p.chunks, p.H, req, i, rows, row0, tok0, h0, len, nullptr)) return;
-    const int tiles = (len + kTile - 1) / kTile, per = (tiles + n - 1) / n;
-    n = (tiles + per - 1) / per;  // splits that have keys
+    n = split_count(len, p.per);
+    if (n == 1) return;  // written already
+    const int tiles = (len + kTile - 1) / kTile, each = (tiles + n - 1) / n;
+    n = (tiles + each - 1) / each;  // splits that have keys
   }
   const int64_t base = (int64_t)tile * p.nsplit * p.prows + r;
   if (threadIdx.x < 32) {
@@ -1115,6 +1183,7 @@ cudaError_t launch(Params p, const MlaArgs& a, int num_sms, cudaStream_t s) {
                              !encode_tmap_2d(&pmap, a.latent.data, 2, kDqk, pool_rows, kDqk * 2, 64, kTile, true)))
     return cudaErrorInvalidValue;
   p.data = static_cast<const uint8_t*>(a.latent.data);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.scale = a.latent.scale;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
@@ -1128,6 +1197,13 @@ cudaError_t launch(Params p, const MlaArgs& a, int num_sms, cudaStream_t s) {
     p.part_o = static_cast<float*>(a.workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
                                           up256((size_t)p.tiles * p.nsplit * p.prows * kDv * sizeof(float)));
+  }
+  // several requests: their units differ in size, and are handed out as CTAs become free
+  p.next = nullptr;
+  if (kSrc != kSelected && p.nsplit > 1 && p.num_reqs > 1) {
+    p.next = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(p.part_lse) + up256((size_t)p.tiles * p.nsplit * p.prows * sizeof(float)));
+    const cudaError_t e = cudaMemsetAsync(p.next, 0, sizeof(int), s);
+    if (e != cudaSuccess) return e;
   }
   const int units = p.tiles * p.nsplit * 2;
   auto kernel = mla_packed_kernel<kSrc>;
@@ -1147,43 +1223,47 @@ int64_t chunk_tiles(int num_tokens, int num_reqs, int H) { return first_tile(num
 
 }  // namespace
 
-// Key splits of a batch of chunks: as many as fill the SMs.  Cost model in key-tile times, as for the
-// sparse kernel: a unit costs its key tiles and a fixed ~3; units run in waves of one per SM; more
-// than one split adds the combine pass.  Only max_context and the numbers of tokens and requests are
-// known here; a request's own length is split evenly on the device.
-int chunk_mla_splits(int num_tokens, int num_reqs, int H, int max_context, int num_sms) {
+// Key tiles of a split of a batch of chunks, at most.  Cost model in key-tile times: a unit costs its key
+// tiles and a fixed ~4 (queries in, output out); units go round robin over the SMs, so on average half a unit is
+// lost at the end; several splits cost the combine's launch and the partials' way to memory and back.  Only
+// max_context and the numbers of tokens and requests are known here; of several requests the mean length is taken as
+// 0.6 of the longest.
+int chunk_mla_split_tiles(int num_tokens, int num_reqs, int H, int max_context, int num_sms) {
   // tiles in use if the tokens are spread evenly over the requests
   const int64_t per_req = ((int64_t)num_tokens * H + (int64_t)num_reqs * kRows - 1) / ((int64_t)num_reqs * kRows);
   const double tiles = (double)per_req * (num_reqs < num_tokens ? num_reqs : num_tokens);
+  const double mean = num_reqs > 1 ? 0.6 : 1.0;
   const int kt = (max_context + kTile - 1) / kTile;
   double best_cost = 1e300;
-  int best = 1;
+  int best = kt;
   for (int n = 1; n <= kMaxSplits && n <= kt; n *= 2) {
     const int per = (kt + n - 1) / n;
-    double units = 2.0 * tiles * n, waves = (double)(int64_t)((units + num_sms - 1) / num_sms);
-    double cost = waves * (per + 3.0);
-    if (n > 1) cost += 3.0 + 0.02 * tiles * n;
+    const double units = 2.0 * tiles * (mean * n > 1.0 ? mean * n : 1.0);
+    double cost = units <= num_sms ? per + 4.0 : (units / num_sms + 0.5) * (per + 4.0);
+    if (n > 1) cost += 3.0 + 0.05 * tiles * n;
     if (cost < best_cost) {
       best_cost = cost;
-      best = n;
+      best = per;
     }
   }
   return best;
 }
 
-size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int nsplit) {
+size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles) {
+  const int nsplit = ((max_context + kTile - 1) / kTile + split_tiles - 1) / split_tiles;
   if (nsplit <= 1) return 0;
   const size_t rows = (size_t)chunk_tiles(num_tokens, num_reqs, H) * nsplit * kRows;
-  return up256(rows * kDv * sizeof(float)) + up256(rows * sizeof(float));
+  return up256(rows * kDv * sizeof(float)) + up256(rows * sizeof(float)) + 256;  // the last for the unit counter
 }
 
-cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int nsplit, int num_sms, cudaStream_t s) {
+cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split_tiles, int num_sms, cudaStream_t s) {
   Params p = {};
   p.chunks = c;
   p.block_table = c.block_table;
   p.T = c.num_tokens;
   p.H = a.H;
-  p.nsplit = nsplit;
+  p.per = split_tiles;
+  p.nsplit = ((c.max_context + kTile - 1) / kTile + split_tiles - 1) / split_tiles;
   p.prows = kRows;
   const int64_t tiles = chunk_tiles(c.num_tokens, c.num_reqs, a.H);
   if (tiles >= 0x7FFFFFFFll) return cudaErrorInvalidValue;
