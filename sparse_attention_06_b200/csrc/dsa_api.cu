@@ -504,11 +504,12 @@ dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v,
   if (!chunk_tensor_cores(q_dtype, H, d_v, d_rope) || !aligned16(q) || !aligned16(out))
     return cuda_status(launch_chunk_mla_generic(a, *chunks, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch", 1);
   const int split = chunk_mla_split_tiles(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, sms);
-  const size_t need = chunk_mla_workspace(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, split);
+  const size_t need = chunk_mla_workspace(chunks->num_tokens, chunks->num_reqs, H, chunks->max_context, split, true);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(DSA_ERR_INVALID_ARG, "chunk mla: workspace missing, too small or not 256-byte aligned%s");
-  return cuda_status(launch_chunk_mla_tc(a, *chunks, split, sms, static_cast<cudaStream_t>(stream)), "dsa_chunk_mla launch",
-                     need > 0 ? 2 : 1);
+  int kernels = 0;
+  const cudaError_t e = launch_chunk_mla_tc(a, *chunks, split, sms, static_cast<cudaStream_t>(stream), &kernels);
+  return cuda_status(e, "dsa_chunk_mla launch", kernels);
 }
 
 size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
@@ -517,7 +518,7 @@ size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return chunk_mla_workspace(num_tokens, num_reqs, H, max_context,
-                             chunk_mla_split_tiles(num_tokens, num_reqs, H, max_context, sms));
+                             chunk_mla_split_tiles(num_tokens, num_reqs, H, max_context, sms), false);
 }
 
 dsa_status dsa_selftest_bounded_wait(int64_t limit_cycles, dsa_stream stream) {

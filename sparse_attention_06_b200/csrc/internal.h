@@ -83,9 +83,10 @@ size_t mla_tc_workspace_bytes(int T, int H, int d_v, int nsplit);
 // tcgen05 path over packed query rows (d_v 512, d_rope 64, bf16 queries): sparse attention over
 // quantised latents (H <= 128; splits and workspace as mla_tc's) and the dense attention of chunks
 cudaError_t launch_mla_quantised_tc(const MlaArgs& a, int nsplit, int num_sms, cudaStream_t s);
-cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split_tiles, int num_sms, cudaStream_t s);
+cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split_tiles, int num_sms, cudaStream_t s,
+                                int* kernels);
 int chunk_mla_split_tiles(int num_tokens, int num_reqs, int H, int max_context, int num_sms);
-size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles);
+size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles, bool least);
 
 // Launch configuration with programmatic stream serialization (the kernel may start while the
 // previous kernel of the stream finishes; every kernel here waits for it with griddepcontrol.wait

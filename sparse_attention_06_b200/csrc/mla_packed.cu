@@ -78,8 +78,9 @@ constexpr int OFF_STATS = OFF_POISON + kMaskSlots * kMaskBytes;   // 1 / l of ea
 constexpr int OFF_MISC = OFF_STATS + kRows * 4;
 constexpr int OFF_UNIT = OFF_MISC + 16;                  // [2] units in hand
 constexpr int OFF_ROWS = OFF_UNIT + 2 * 40;                  // quantised: [slot][64] pool row of each key of a tile, -1: none to see;
-                                                         // bf16: [slot] page of the tile, then [2][2][128] row maxima exchanged
-constexpr int SMEM = OFF_ROWS + kRowSlots * 4 + 2 * 2 * kRows * 4;
+                                                         // bf16: [slot] page of the tile and its rows that may be read,
+                                                         // then [2][2][128] row maxima exchanged
+constexpr int SMEM = OFF_ROWS + kRowSlots * 16 + 2 * 2 * kRows * 4;
 static_assert(kRowSlots * kTile * 4 <= 2 * 2 * kRows * 4, "row ring");
 static_assert(SMEM <= 232448, "shared memory budget");
 static_assert(kYStages * kYBlocks * K_CHUNK == 3 * Q_CHUNK && kXBlocks * K_CHUNK == Q_CHUNK && kVBlocks * K_CHUNK == 2 * Q_CHUNK,
@@ -121,6 +122,8 @@ struct Params {
   __nv_bfloat16* out;     // [T, H, 512]
   float* lse;             // [T, H] or null
   float *part_o, *part_lse;  // several splits: [tiles, nsplit, prows, 512] and [tiles, nsplit, prows]
+  const uint8_t* row_ok;  // kPagesBf16 over expanded rows: [requests, linear_pages * 64] rows with good scales
+  int linear_pages;       // ... whose pages follow each other, so many for each request; 0: pages of the pool
   int32_t num_blocks, oob_row;
   int T, H, k, ks, nsplit, per, prows, tiles, num_reqs, max_blocks, max_context;
   int* next;              // units handed out beyond the first of each CTA (zero at launch), or null: round robin
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
   uint64_t* r_empty = bars + 24;    // [kRowSlots] ... read by the fill warps
   uint8_t* masks = smem + OFF_MASK;
   int32_t* row_ring = reinterpret_cast<int32_t*>(smem + OFF_ROWS);
-  float* row_max = reinterpret_cast<float*>(smem + OFF_ROWS + kRowSlots * 4);
+  float* row_max = reinterpret_cast<float*>(smem + OFF_ROWS + kRowSlots * 16);
   uint64_t* u_full = bars + 32;     // [kUnitSlots] a unit (or the end) published
   uint64_t* u_empty = bars + 34;    // [kUnitSlots] ... taken by every warp that works on it
   Unit* unit_ring = reinterpret_cast<Unit*>(smem + OFF_UNIT);
@@ -687,8 +690,9 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
           if (lane == 0) mbar_arrive(&k_full[s]);
         } else {
           if (!(ok = wait_rows(gi))) break;
-          const int page = row_ring[gi % kRowSlots], key = warp * kKeysPerWarp + (lane & 7);
-          const int row = page >= 0 && x.lo + j * kTile + key < x.hi ? page * kTile + key : -1;
+          const int page = row_ring[gi % kRowSlots * 4], key = warp * kKeysPerWarp + (lane & 7);
+          const bool may = ((uint32_t)row_ring[gi % kRowSlots * 4 + 2 + (key >> 5)] >> (key & 31)) & 1u;
+          const int row = page >= 0 && may && x.lo + j * kTile + key < x.hi ? page * kTile + key : -1;
           const uint32_t valid = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
           if (lane == 0) mbar_arrive(&r_empty[gi % kRowSlots]);
           const int base = x.lo + j * kTile;
@@ -1041,9 +1045,18 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
               if (report) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
               page = -1;
             }
+            uint32_t may[2] = {~0u, ~0u};
+            if (p.linear_pages && page >= 0) {
+              page = x.req * p.linear_pages + lblk;
+              const uint8_t* f = p.row_ok + (int64_t)page * kTile;
+              may[0] = __ballot_sync(0xFFFFFFFFu, f[lane] != 0);
+              may[1] = __ballot_sync(0xFFFFFFFFu, f[lane + 32] != 0);
+            }
             if (gi >= kRowSlots && !(ok = warp_wait(&r_empty[gi % kRowSlots], ((gi / kRowSlots) - 1) & 1, p.err, abort_flag))) break;
             if (lane == 0) {
-              row_ring[gi % kRowSlots] = page;
+              row_ring[gi % kRowSlots * 4] = page;
+              row_ring[gi % kRowSlots * 4 + 2] = (int32_t)may[0];
+              row_ring[gi % kRowSlots * 4 + 3] = (int32_t)may[1];
               mbar_arrive(&r_full[gi % kRowSlots]);
             }
           }
@@ -1168,26 +1181,69 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
   if (p.lse && threadIdx.x == 0) p.lse[row] = s_lse;
 }
 
+// Quantised rows of a batch of chunks as bf16 rows, once, for row tiles that would each turn them into bf16 again:
+// a quantised key tile costs the attention ~4000 cycles, a bf16 one ~2500.  One warp per position of a request that
+// has tokens; rows[(request, position)], rows of pages outside the pool are left out (never read).
+constexpr int kExpandWarps = 4;
+__global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const uint8_t* data, const float* scale, int num_blocks,
+                                                                   const dsa_chunks c, int linear_pages, __nv_bfloat16* rows,
+                                                                   uint8_t* row_ok, int* err) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int per_req = linear_pages * kTile;
+  const int64_t i = (int64_t)blockIdx.x * kExpandWarps + (threadIdx.x >> 5);
+  const int r = (int)(i / per_req), pos = (int)(i % per_req);
+  if (r >= c.num_reqs || pos >= c.max_context || pos >= c.seq_len[r] || c.cu_tokens[r + 1] <= c.cu_tokens[r]) return;
+  const int32_t blk = c.block_table[(int64_t)r * c.max_blocks + pos / kTile];
+  if (blk < 0 || blk >= num_blocks) return;
+  const int64_t row = (int64_t)blk * kTile + pos % kTile;
+  const uint8_t* src = data + row * kLatentBytes;
+  uint2 w[2];
+  float s[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = __ldg(reinterpret_cast<const uint2*>(src + 256 * h) + lane);
+    s[h] = __ldg(scale + row * 4 + 2 * h + (lane >> 4));
+  }
+  uint4 rope;
+  if (lane < 8) rope = __ldg(reinterpret_cast<const uint4*>(src + kDv) + lane);
+  const bool ok = __all_sync(0xFFFFFFFFu, latent_scale_ok(s[0]) && latent_scale_ok(s[1]));
+  if (lane == 0) {
+    row_ok[i] = ok;
+    if (!ok) raise_error(err, DSA_DEVERR_SCALE);
+  }
+  if (!ok) return;
+  uint4* dst = reinterpret_cast<uint4*>(rows + i * kDqk);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t b[4];
+    decode4(w[h].x, make_float2(s[h], s[h]), b[0], b[1]);
+    decode4(w[h].y, make_float2(s[h], s[h]), b[2], b[3]);
+    dst[32 * h + lane] = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+  if (lane < 8) dst[64 + lane] = rope;
+}
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <Source kSrc>
-cudaError_t launch(Params p, const MlaArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch(Params p, const MlaArgs& a, const void* data, int num_blocks, int num_sms, cudaStream_t s) {
   alignas(64) CUtensorMap qmap = {}, rmap = {}, pmap = {};
   if (!encode_tmap_2d(&qmap, a.q, 2, kDqk, (uint64_t)p.T * p.H, kDqk * 2, 64, kRows, true)) return cudaErrorInvalidValue;
-  const uint64_t pool_rows = (uint64_t)a.latent.num_blocks * kTile;
+  const uint64_t pool_rows = (uint64_t)num_blocks * kTile;  // of the rows that are copied
   // row numbers are 32-bit
   if (pool_rows >= 0x7FFFFFFFull || (int64_t)p.T * p.H + kRows >= 0x7FFFFFFFll ||
       (int64_t)p.tiles * p.nsplit * p.prows >= 0x7FFFFFFFll || (int64_t)p.tiles * p.nsplit * 2 >= 0x7FFFFFFFll)
     return cudaErrorInvalidValue;
-  if (kSrc == kPagesBf16 && (!encode_tmap_2d(&rmap, a.latent.data, 2, kDqk, pool_rows, kDqk * 2, 64, 1, true) ||
-                             !encode_tmap_2d(&pmap, a.latent.data, 2, kDqk, pool_rows, kDqk * 2, 64, kTile, true)))
+  if (kSrc == kPagesBf16 && (!encode_tmap_2d(&rmap, data, 2, kDqk, pool_rows, kDqk * 2, 64, 1, true) ||
+                             !encode_tmap_2d(&pmap, data, 2, kDqk, pool_rows, kDqk * 2, 64, kTile, true)))
     return cudaErrorInvalidValue;
-  p.data = static_cast<const uint8_t*>(a.latent.data);
+  p.data = static_cast<const uint8_t*>(data);
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.scale = a.latent.scale;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.num_blocks = a.latent.num_blocks;
   p.oob_row = (int32_t)pool_rows;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.err = a.err;
@@ -1249,14 +1305,36 @@ int chunk_mla_split_tiles(int num_tokens, int num_reqs, int H, int max_context, 
   return best;
 }
 
-size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles) {
-  const int nsplit = ((max_context + kTile - 1) / kTile + split_tiles - 1) / split_tiles;
-  if (nsplit <= 1) return 0;
-  const size_t rows = (size_t)chunk_tiles(num_tokens, num_reqs, H) * nsplit * kRows;
-  return up256(rows * kDv * sizeof(float)) + up256(rows * sizeof(float)) + 256;  // the last for the unit counter
+namespace {
+// Of a call with these sizes: the partials of split row tiles (and the unit counter), which it cannot do without, and
+// the room for expanded rows, which it uses where there are quantised ones.
+struct ChunkWorkspace {
+  size_t partials, rows, total;
+  int linear_pages;
+};
+ChunkWorkspace chunk_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles) {
+  ChunkWorkspace w = {0, 0, 0, (max_context + kTile - 1) / kTile};
+  const int nsplit = (w.linear_pages + split_tiles - 1) / split_tiles;
+  if (nsplit > 1) {
+    const size_t rows = (size_t)chunk_tiles(num_tokens, num_reqs, H) * nsplit * kRows;
+    w.partials = up256(rows * kDv * sizeof(float)) + up256(rows * sizeof(float)) + 256;
+  }
+  // worth it from about three row tiles per request on (each key tile then saves at least six times ~1500 cycles for
+  // ~3.5 MB/us of memory traffic spread over all SMs); bounded, since it grows with the contexts
+  const size_t rows = (size_t)num_reqs * w.linear_pages * kTile;
+  if ((int64_t)num_tokens * H > (int64_t)2 * kRows * num_reqs && rows * kDqk * 2 <= (256u << 20))
+    w.rows = up256(rows * kDqk * 2) + up256(rows);
+  w.total = w.partials + w.rows;
+  return w;
+}
+}  // namespace
+
+size_t chunk_mla_workspace(int num_tokens, int num_reqs, int H, int max_context, int split_tiles, bool least) {
+  const ChunkWorkspace w = chunk_workspace(num_tokens, num_reqs, H, max_context, split_tiles);
+  return least ? w.partials : w.total;
 }
 
-cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split_tiles, int num_sms, cudaStream_t s) {
+cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split_tiles, int num_sms, cudaStream_t s, int* kernels) {
   Params p = {};
   p.chunks = c;
   p.block_table = c.block_table;
@@ -1271,7 +1349,25 @@ cudaError_t launch_chunk_mla_tc(const MlaArgs& a, const dsa_chunks& c, int split
   p.num_reqs = c.num_reqs;
   p.max_blocks = c.max_blocks;
   p.max_context = c.max_context;
-  return a.latent.dtype == DSA_BF16 ? launch<kPagesBf16>(p, a, num_sms, s) : launch<kPages>(p, a, num_sms, s);
+  const void* data = a.latent.data;
+  const int blocks = a.latent.num_blocks;
+  p.num_blocks = blocks;
+  *kernels = p.nsplit > 1 ? 2 : 1;
+  if (a.latent.dtype == DSA_BF16) return launch<kPagesBf16>(p, a, data, blocks, num_sms, s);
+  const ChunkWorkspace w = chunk_workspace(c.num_tokens, c.num_reqs, a.H, c.max_context, split_tiles);
+  if (!w.rows || a.workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)) return launch<kPages>(p, a, data, blocks, num_sms, s);
+  const int64_t rows = (int64_t)c.num_reqs * w.linear_pages * kTile;
+  uint8_t* at = static_cast<uint8_t*>(a.workspace) + w.partials;
+  p.linear_pages = w.linear_pages;
+  uint8_t* row_ok = at + up256((size_t)rows * kDqk * 2);
+  p.row_ok = row_ok;
+  cudaLaunchAttribute attrs[2];
+  const cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)((rows + kExpandWarps - 1) / kExpandWarps)), dim3(32 * kExpandWarps), 0, s, attrs);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, (const uint8_t*)data, a.latent.scale, blocks, c, w.linear_pages,
+                                           reinterpret_cast<__nv_bfloat16*>(at), row_ok, a.err);
+  if (e != cudaSuccess) return e;
+  ++*kernels;
+  return launch<kPagesBf16>(p, a, at, c.num_reqs * w.linear_pages, num_sms, s);
 }
 
 cudaError_t launch_mla_quantised_tc(const MlaArgs& a, int nsplit, int num_sms, cudaStream_t s) {
@@ -1288,7 +1384,8 @@ cudaError_t launch_mla_quantised_tc(const MlaArgs& a, int nsplit, int num_sms, c
   p.num_reqs = a.batch.num_reqs;
   p.max_blocks = a.batch.max_blocks;
   p.max_context = a.batch.max_context;
-  return launch<kSelected>(p, a, num_sms, s);
+  p.num_blocks = a.latent.num_blocks;
+  return launch<kSelected>(p, a, a.latent.data, a.latent.num_blocks, num_sms, s);
 }
 
 }  // namespace dsa
