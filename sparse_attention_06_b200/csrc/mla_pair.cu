@@ -1,0 +1,744 @@
+// mla_pair.cu -- dense MLA (MQA mode) of chunks of new tokens over bf16 rows, a CTA pair to a tile of 128
+// query rows (mla_packed.cu has the packing of query rows, and the quantised sources).
+//
+// O of 128 rows x 512 values in f32 fills tensor memory, so the values are split over two CTAs; if each computed
+// S = Q K^T for itself, 576 of 1088 multiplications would be done twice.  Here the two are a cluster: of every
+// 128 keys (a step) each computes S and P for its own 64-key page, and hands P to the other through distributed
+// shared memory (16 KB a step); both multiply the whole P (128 rows x 128 keys) with their half of the values.
+// Softmax bases have to agree: the rows' maxima of the two pages are exchanged first (one f32 a row).
+//
+// Per step and CTA: Q K^T of 64 keys (36 products of N = 64, ~1340 cycles), P V of 128 keys (8 of N = 256, 1024), into
+// shared memory the own page's nine 64-dim column blocks (72 KB) and this half's four of the other page (32 KB).
+//
+// Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
+// three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
+// them, and a ring of three V stages (32 KB: four value blocks of a page, needed until its P V is done), used in the
+// order own page of step 0, other page of step 0, own page of step 1, ...
+//
+// Roles (16 warps): 0-7 copy (TMA: whole pages as 64-row boxes, a page's visible part by gather4) and move Q into
+// tensor memory; 8-11 softmax and epilogue, one row per thread; 12 issues the products; 13 hands out units and looks
+// pages up.  Order of products: Q K^T of step g, then P V of step g - 1, so that the tensor core has P V to do while the
+// softmax reads S.  All waits are bounded; bad rows set the device error word and are skipped.
+#include "mla_packed.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace packed;
+
+constexpr int kVStages = 3;
+constexpr int kIssueWarp = kFillWarps + 4, kLookupWarp = kIssueWarp + 1;
+constexpr int kThreads = 32 * 16;
+// registers a thread by warpgroup: 2 x 96 + 184 + 136 = 4 x 128
+constexpr int kFillRegs = 96, kSoftmaxRegs = 184, kIssueRegs = 136;
+
+constexpr int P_BYTES = kRows * kTile * 2;
+constexpr int V_BYTES = kVBlocks * K_CHUNK;
+constexpr int OFF_Q = 0;
+constexpr int OFF_P = OFF_Q + kSmemQ * Q_CHUNK;            // [2]: of the page of CTA 0, of CTA 1
+constexpr int OFF_Y = OFF_P + 2 * P_BYTES;
+constexpr int OFF_X = OFF_Y + kYBlocks * K_CHUNK;
+constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;
+constexpr int OFF_BAR = OFF_V + kVStages * V_BYTES;
+constexpr int NBAR = 48;
+constexpr int kSlots = 4;
+constexpr int OFF_MASK = OFF_BAR + NBAR * 8;               // [slot] keys of the own page with a row to see, a byte per fill warp
+constexpr int OFF_POISON = OFF_MASK + kSlots * 8;          // [slot] rows with NaN or infinity, see below
+constexpr int OFF_STATS = OFF_POISON + kSlots * 8;         // 1 / l of each row (last unit)
+constexpr int OFF_MAX = OFF_STATS + kRows * 4;             // [2][128] values of the other CTA's rows
+constexpr int OFF_UNIT = OFF_MAX + 2 * kRows * 4;          // [2] units in hand
+constexpr int OFF_ROWS = OFF_UNIT + kUnitSlots * 40;       // [slot] own page, other page, masks of their rows that may be read
+constexpr int OFF_MAIL = OFF_ROWS + kSlots * 32;           // [4] units from CTA 0
+constexpr int OFF_MISC = OFF_MAIL + 16;
+constexpr int SMEM = OFF_MISC + 16;
+static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(OFF_ROWS % 16 == 0 && OFF_MASK % 8 == 0, "alignment");
+
+// ---- cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(const void* mine, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  return a;
+}
+// stores into the other CTA whose bytes are counted on its barrier `bar` once they are there
+__device__ __forceinline__ void st_async4(uint32_t dst, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst), "r"(v), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_async16(uint32_t dst, uint4 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+               : "memory");
+}
+// warp-collective bounded wait for a phase that bytes from the other CTA complete
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, err, abort_flag);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+// arrive on `bar` of both CTAs once every product issued so far by this thread has completed
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
+                    const __grid_constant__ CUtensorMap pmap, const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t v = cluster_rank();  // this CTA's value half, and its page of each step
+  uint8_t* q_s = smem + OFF_Q;
+  uint8_t* x_st = smem + OFF_X;
+  uint8_t* y_st = smem + OFF_Y;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* xy_full = bars + 0;     // [2] X and Y of the own page in place, masks published
+  uint64_t* vo_full = bars + 2;     // [2] V of the own page
+  uint64_t* vp_full = bars + 4;     // [2] V of the other page
+  uint64_t* land = bars + 6;        // [2] rows landed, to be looked over before the above: own page
+  uint64_t* land_p = bars + 8;      // [2] other page
+  uint64_t* x_empty = bars + 10;    // Q K^T is past the X blocks
+  uint64_t* y_empty = bars + 11;    // ... past the Y blocks
+  uint64_t* v_empty = bars + 12;    // [kVStages] P V of the stage done
+  uint64_t* q_stage = bars + 15;
+  uint64_t* q_read = bars + 16;
+  uint64_t* q_full = bars + 17;
+  uint64_t* q_empty = bars + 18;
+  uint64_t* s_full = bars + 19;
+  uint64_t* s_empty = bars + 20;
+  uint64_t* p_full = bars + 21;     // P of both pages written (the other CTA's counted in bytes)
+  uint64_t* pv_done = bars + 22;    // P V of the step done, in both CTAs
+  uint64_t* fin = bars + 23;
+  uint64_t* ep_last = bars + 24;
+  uint64_t* r_full = bars + 25;     // [kSlots]
+  uint64_t* r_empty = bars + 29;    // [kSlots]
+  uint64_t* u_full = bars + 33;     // [kUnitSlots]
+  uint64_t* u_empty = bars + 35;    // [kUnitSlots]
+  uint64_t* x_bar = bars + 37;      // [4] the other CTA's values of 32 rows have come
+  uint64_t* mail = bars + 41;       // [4] a unit from CTA 0 has come
+  uint8_t* masks = smem + OFF_MASK;
+  uint8_t* poisons = smem + OFF_POISON;
+  float* stats = reinterpret_cast<float*>(smem + OFF_STATS);
+  volatile float* peer_max = reinterpret_cast<volatile float*>(smem + OFF_MAX);
+  Unit* unit_ring = reinterpret_cast<Unit*>(smem + OFF_UNIT);
+  int32_t* row_ring = reinterpret_cast<int32_t*>(smem + OFF_ROWS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = p.tiles * p.nsplit, clusters = gridDim.x / 2;
+  griddep_launch_dependents();
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&xy_full[i], kFillWarps);
+      mbar_init(&vo_full[i], kFillWarps);
+      mbar_init(&vp_full[i], kFillWarps);
+      mbar_init(&land[i], kFillWarps);
+      mbar_init(&land_p[i], kFillWarps);
+    }
+    mbar_init(x_empty, 1);
+    mbar_init(y_empty, 1);
+    for (int i = 0; i < kVStages; ++i) mbar_init(&v_empty[i], 1);
+    mbar_init(q_stage, 1);
+    mbar_init(q_read, kFillWarps);
+    mbar_init(q_full, kFillWarps);
+    mbar_init(q_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 2);
+    mbar_init(fin, 1);
+    mbar_init(ep_last, 4);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_empty[i], kFillWarps);
+      mbar_init(&x_bar[i], 1);
+      mbar_init(&mail[i], 1);
+    }
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], kIssueWarp + 1);  // fill, softmax, issue
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(tmem_slot, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+
+  auto take_unit = [&](int k, Unit& x) -> bool {
+    if (!warp_wait(&u_full[k % kUnitSlots], (k / kUnitSlots) & 1, p.err, abort_flag)) return false;
+    x = unit_ring[k % kUnitSlots];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[k % kUnitSlots]);
+    return x.rows > 0;
+  };
+  auto last_unit = [&](int k, bool& last) -> bool {
+    if (!warp_wait(&u_full[(k + 1) % kUnitSlots], ((k + 1) / kUnitSlots) & 1, p.err, abort_flag)) return false;
+    last = unit_ring[(k + 1) % kUnitSlots].rows < 0;
+    return true;
+  };
+  auto v_stage = [&](int item) { return smem + OFF_V + item % kVStages * V_BYTES; };
+
+  if (warp < kFillWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
+    // ------------------------------------------------------------------ copies, and Q into tensor memory
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int key = warp * kKeysPerWarp + (lane & 7);
+    int gi = 0, ui = 0;  // steps and units of this CTA
+    uint32_t nland[2] = {0u, 0u}, nland_p[2] = {0u, 0u};
+    bool ok = true, staged = false;
+    Unit x;
+    for (; ok && take_unit(ui, x);) {
+      const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+
+      // --- Q of the unit: places 0 .. 2 of the block order to shared memory, the other six through X, the
+      // first two thirds of Y and the two V stages next in turn to tensor memory
+      uint8_t* stage_at[6] = {x_st, y_st, v_stage(2 * gi), v_stage(2 * gi) + Q_CHUNK, v_stage(2 * gi + 1), v_stage(2 * gi + 1) + Q_CHUNK};
+      auto v_free = [&](int item) {
+        return item < kVStages || warp_wait(&v_empty[item % kVStages], ((item / kVStages) - 1) & 1, p.err, abort_flag);
+      };
+      if (ui >= 1 && !(ok = warp_wait(q_empty, (ui - 1) & 1, p.err, abort_flag))) break;
+      if (!(ok = v_free(2 * gi)) || !(ok = v_free(2 * gi + 1))) break;
+      if (tid == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(q_stage, kChunks * Q_CHUNK);
+#pragma unroll
+        for (int c = kSmemQ; c < kChunks; ++c) tma_load_2d(stage_at[c - kSmemQ], &qmap, q_stage, block_of(c, v) * 64, x.row0);
+        for (int c = 0; c < kSmemQ; ++c) tma_load_2d(q_s + c * Q_CHUNK, &qmap, q_stage, block_of(c, v) * 64, x.row0);
+        staged = true;
+      }
+      tc_fence_after();
+      if (!(ok = warp_wait(q_stage, ui & 1, p.err, abort_flag))) break;
+      staged = false;
+      {
+        const int r = quarter * 32 + lane;
+#pragma unroll
+        for (int b = 0; b < 6; ++b) {  // this warp's half (64 bytes) of the row's block
+          const uint8_t* src = stage_at[b] + r * 128;
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + (((part * 4 + e) ^ (r & 7)) << 4));
+            w[4 * e] = y.x; w[4 * e + 1] = y.y; w[4 * e + 2] = y.z; w[4 * e + 3] = y.w;
+          }
+          tmem_st16(my_lanes + TM_Q + b * 32 + part * 16, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(q_full);
+        mbar_arrive(q_read);
+      }
+      if (!(ok = warp_wait(q_read, ui & 1, p.err, abort_flag))) break;
+      ++ui;
+
+      // --- copies.  A page: its first position, its number (-1: none), its rows that may be read.
+      struct Page {
+        int base, page;
+        uint32_t may[2];
+      };
+      auto page_of = [&](int g, int j, int which) -> Page {  // which: 0 own, 1 the other
+        const int32_t* e = row_ring + g % kSlots * 8;
+        return Page{x.lo + (2 * j + (which ? 1 - (int)v : (int)v)) * kTile, e[which], {(uint32_t)e[2 + 2 * which], (uint32_t)e[3 + 2 * which]}};
+      };
+      auto row_of = [&](const Page& a) -> int {
+        const bool may = (a.may[key >> 5] >> (key & 31)) & 1u;
+        return a.page >= 0 && may && a.base + key < x.hi ? a.page * kTile + key : -1;
+      };
+      auto is_whole = [&](const Page& a) { return a.page >= 0 && (a.may[0] & a.may[1]) == ~0u && a.base + kTile <= x.hi; };
+      // rows that only some of the tile's tokens see: a NaN there must not reach the others through 0 * NaN in P V
+      auto is_partly = [&](const Page& a) { return a.base + kTile - 1 > x.tok0 && x.hi - 1 > max(x.tok0, a.base - 1); };
+      auto arm = [&](uint64_t* bar, bool whole, int blocks) {
+        if (lane != 0) return;
+        if (!whole)
+          mbar_arrive_expect_tx(bar, kKeysPerWarp * 128 * blocks);
+        else if (warp == 0)
+          mbar_arrive_expect_tx(bar, K_CHUNK * blocks);
+        else
+          mbar_arrive(bar);
+      };
+      // places lo .. hi - 1 of the block order
+      auto copy = [&](const Page& a, bool whole, int row, int lo, int hi, uint8_t* dst, uint64_t* bar) {
+        if (whole) {
+          if (warp == 0 && lane == 0)
+            for (int c = lo; c < hi; ++c) tma_load_2d(dst + (c - lo) * K_CHUNK, &pmap, bar, block_of(c, v) * 64, a.page * kTile);
+          return;
+        }
+#pragma unroll
+        for (int g4 = 0; g4 < 2; ++g4) {
+          const int rc = row >= 0 ? row : p.oob_row;
+          const int r0 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4), r1 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 1);
+          const int r2 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 2), r3 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 3);
+          if (lane == 0)
+            for (int c = lo; c < hi; ++c)
+              tma_gather4(dst + (c - lo) * K_CHUNK + (warp * kKeysPerWarp + 4 * g4) * 128, &rmap, bar, block_of(c, v) * 64, r0, r1, r2, r3);
+        }
+      };
+      // Looks over one 64-dim block's 128 bytes of eight rows (four lanes a row): whether values are not finite; `zero`
+      // makes those zero.  Returns a bit per row of this warp.
+      auto scan = [&](const Page& a, uint8_t* block, bool zero) -> uint32_t {
+        const int r = warp * kKeysPerWarp + (lane >> 2);
+        bool f = false;
+        if (a.base + r > x.tok0 && a.base + r < x.hi) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint4* at = reinterpret_cast<uint4*>(block + r * 128 + (((lane & 3) * 2 + e) << 4));
+            const uint4 y = *at;
+            uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            bool g = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; g = true; }
+              if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; g = true; }
+            }
+            if (g && zero) *at = make_uint4(w[0], w[1], w[2], w[3]);
+            f |= g;
+          }
+        }
+        const uint32_t b = __ballot_sync(0xFFFFFFFFu, f);
+        uint32_t rows = 0u;
+#pragma unroll
+        for (int k = 0; k < kKeysPerWarp; ++k) rows |= (b >> (4 * k)) & 0xFu ? 1u << k : 0u;
+        return rows;
+      };
+      // the other page's V of step j (CTA step g)
+      Page peer = {0, -1, {0u, 0u}};
+      auto copy_peer = [&](int g) -> bool {
+        const int item = 2 * g + 1, s = g & 1;
+        const bool whole = is_whole(peer), partly = is_partly(peer);
+        if (!v_free(item)) return false;
+        uint64_t* bar = partly ? &land_p[s] : &vp_full[s];
+        if (lane == 0) fence_proxy_async_smem();
+        arm(bar, whole, kVBlocks);
+        __syncwarp();
+        copy(peer, whole, row_of(peer), 5, 9, v_stage(item), bar);
+        if (partly) {
+          if (!warp_wait(&land_p[s], nland_p[s] & 1, p.err, abort_flag)) return false;
+          ++nland_p[s];
+          for (int c = 0; c < kVBlocks; ++c) scan(peer, v_stage(item) + c * K_CHUNK, true);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vp_full[s]);
+        }
+        return true;
+      };
+
+      // Order by when the places become free: X and Y of step g while Q K^T of g - 1 runs, then, as P V of g - 2 goes
+      // on, V of the other page of g - 1 and of the own page of g.
+      for (int j = 0; j < nsteps; ++j, ++gi) {
+        const int s = gi & 1, slot = gi % kSlots;
+        if (!(ok = warp_wait(&r_full[slot], (gi / kSlots) & 1, p.err, abort_flag))) break;
+        const Page own = page_of(gi, j, 0), next_peer = page_of(gi, j, 1);
+        const int row = row_of(own);
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFu;
+        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        const bool whole = is_whole(own), partly = is_partly(own);
+        uint64_t* xy_bar = partly ? &land[s] : &xy_full[s];
+        uint64_t* vo_bar = partly ? &land[s] : &vo_full[s];
+        if (gi >= 1 && !(ok = warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag))) break;
+        if (lane == 0) {
+          masks[slot * 8 + warp] = (uint8_t)valid;
+          if (!partly) poisons[slot * 8 + warp] = 0;
+          fence_proxy_async_smem();
+        }
+        arm(xy_bar, whole, partly ? kChunks : kXBlocks + kYBlocks);
+        __syncwarp();
+        copy(own, whole, row, 0, 2, x_st, xy_bar);
+        if (gi >= 1 && !(ok = warp_wait(y_empty, (gi - 1) & 1, p.err, abort_flag))) break;
+        copy(own, whole, row, 2, 5, y_st, xy_bar);
+        if (j > 0 && !(ok = copy_peer(gi - 1))) break;
+        peer = next_peer;
+        if (!(ok = v_free(2 * gi))) break;
+        if (!partly) arm(vo_bar, whole, kVBlocks);
+        __syncwarp();
+        copy(own, whole, row, 5, 9, v_stage(2 * gi), vo_bar);
+        if (partly) {
+          if (!(ok = warp_wait(&land[s], nland[s] & 1, p.err, abort_flag))) break;
+          ++nland[s];
+          // values that are not finite become zero in the V blocks and their row is noted: the softmax makes
+          // the weights of the tokens that see it NaN.  (In X and Y a NaN only reaches logits, of hidden keys masked ones.)
+          uint32_t poison = 0u;
+          for (int c = 0; c < kVBlocks; ++c) poison |= scan(own, v_stage(2 * gi) + c * K_CHUNK, true);
+          poison |= scan(own, x_st + K_CHUNK, false);
+          for (int c = 0; c < kYBlocks; ++c) poison |= scan(own, y_st + c * K_CHUNK, false);
+          if (lane == 0) poisons[slot * 8 + warp] = (uint8_t)poison;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&xy_full[s]);
+            mbar_arrive(&vo_full[s]);
+          }
+        }
+      }
+      if (ok) ok = copy_peer(gi - 1);
+      bool last;
+      if (!ok || !(ok = last_unit(ui - 1, last))) break;
+      if (last) {
+        if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
+        tc_fence_after();
+        store_o(p, x, my_lanes, quarter, 64 + 96 * part, 160 + 96 * part, smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], true);
+        tc_fence_before();
+      }
+    }
+    // gave up: copies in flight must land before the CTA exits
+    if (!ok && staged) mbar_wait(q_stage, ui & 1, p.err, nullptr);
+    if (!ok && lane == 0) {
+      for (int t = gi > 0 ? gi - 1 : 0; t <= gi; ++t) {
+        mbar_wait(&xy_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr, kWaitCycles / 16);
+        mbar_wait(&vo_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr, kWaitCycles / 16);
+        mbar_wait(&vp_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr, kWaitCycles / 16);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_wait(&land[i], nland[i] & 1, p.err, nullptr, kWaitCycles / 16);
+        mbar_wait(&land_p[i], nland_p[i] & 1, p.err, nullptr, kWaitCycles / 16);
+      }
+    }
+  } else if (warp < kIssueWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------------------------ softmax and epilogue
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t peer_x_bar = peer_address(&x_bar[quarter], v ^ 1u), peer_p_full = peer_address(p_full, v ^ 1u);
+    uint8_t* p_row = smem + OFF_P + v * P_BYTES + (r >> 3) * 1024 + (r & 7) * 16;
+    const uint32_t peer_p_row = peer_address(p_row, v ^ 1u);
+    const uint32_t peer_slot = peer_address(smem + OFF_MAX + r * 4, v ^ 1u);
+    int gi = 0, nx = 0;
+    bool ok = true;
+    // The other CTA's value of this row.  The barrier is armed before the own value goes out: the other CTA, which waits
+    // for it, cannot be a round ahead.
+    auto exchange = [&](float mine, float& other) -> bool {
+      if (lane == 0) mbar_arrive_expect_tx(&x_bar[quarter], 128);
+      __syncwarp();
+      const int buf = (nx & 1) * kRows;
+      st_async4(peer_slot + buf * 4, __float_as_uint(mine), peer_x_bar);
+      if (!cluster_wait(&x_bar[quarter], nx & 1, p.err, abort_flag)) return false;
+      ++nx;
+      other = peer_max[buf + r];
+      return true;
+    };
+    Unit x;
+    for (int ui = 0; ok && take_unit(ui, x); ++ui) {
+      const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+      const int limit = r < x.rows ? x.tok0 + (x.h0 + r) / p.H : -1;  // last position this row sees
+      float m_used = -INFINITY, l = 0.0f;
+      for (int j = 0; j < nsteps; ++j, ++gi) {
+        const int slot = gi % kSlots;
+        if (!(ok = warp_wait(s_full, gi & 1, p.err, abort_flag))) break;
+        if (!(ok = warp_wait(&xy_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;  // (long past: orders the masks)
+        tc_fence_after();
+        uint32_t sv[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld16(lane_base + TM_S + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * c]));
+        uint64_t valid = *reinterpret_cast<const volatile uint64_t*>(masks + slot * 8);
+        const uint64_t poison = *reinterpret_cast<const volatile uint64_t*>(poisons + slot * 8);
+        const int d = limit - (x.lo + (2 * j + (int)v) * kTile);  // this row sees the page's keys 0 .. d
+        if (d < 63) valid &= d < 0 ? 0ull : (2ull << d) - 1ull;
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        if (!__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            if ((poison >> c) & 1u) sv[c] = 0x7FC00000u;
+            if (!((valid >> c) & 1u)) sv[c] = 0xFF800000u;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(sv[c]);
+#pragma unroll
+        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        float other;
+        if (!(ok = exchange(mt, other))) break;
+        mt = fmaxf(mt, other);
+        // Lazy rescale: a row's base m_used moves only when its maximum exceeds it by more than 2^8 (P stays
+        // <= 256); the warp takes the step together, since the tensor-memory accesses are warp-collective.
+        const bool rescale = __any_sync(0xFFFFFFFFu, mt > m_used + 8.0f);
+        float f = 1.0f;
+        if (rescale) {
+          const float m_new = mt > m_used + 8.0f ? mt : m_used;  // (a row's base depends on that row alone)
+          f = m_new == -INFINITY ? 1.0f : exp2f(m_used - m_new);  // 0 when m_used = -inf
+          l *= f;
+          m_used = m_new;
+        }
+        uint32_t pk[32];
+        const float nsub = m_used == -INFINITY ? 0.0f : -m_used;
+        float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), ns2 = make_float2(nsub, nsub);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 e = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, ns2);
+          const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+          // (the normaliser sums the weights before their rounding to bf16, which P V needs)
+          ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], w);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
+          pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        const float2 pt = add2(ps[0], ps[1]);
+        l += pt.x + pt.y;
+        // O and both CTAs' P buffers are free once the previous step's P V has completed in both
+        if (gi >= 1 && !(ok = cluster_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+#pragma unroll
+        for (int kc = 0; kc < 8; ++kc) {
+          const uint4 y = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
+          st_async16(peer_p_row + kc * 128, y, peer_p_full);
+          *reinterpret_cast<uint4*>(p_row + kc * 128) = y;
+        }
+        if (rescale && j > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < kHalf; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_ld16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st16(lane_base + TM_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_st16(lane_base + TM_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+          }
+          tmem_wait_st();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(p_full, 32 * 128);  // and the other CTA's P of these 32 rows
+      }
+      if (!ok) break;
+      float other;
+      if (!(ok = exchange(l, other))) break;
+      l = v ? other + l : l + other;
+      if (!(ok = cluster_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+      tc_fence_after();
+      // a row that saw nothing: 0 and -inf; NaN stays NaN
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float lse = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+      bool last;
+      if (!(ok = last_unit(ui, last))) break;
+      if (last) {
+        stats[r] = inv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ep_last);
+      }
+      store_o(p, x, lane_base, quarter, 0, last ? 64 : kHalf, smem + OFF_P + v * P_BYTES + quarter * 2048, inv, true);
+      if (v == 0 && r < x.rows) {
+        if (x.splits == 1) {
+          if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;
+        } else {
+          p.part_lse[(int64_t)x.prow + r] = lse;
+        }
+      }
+      tc_fence_before();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == kIssueWarp) {
+      // ------------------------------------------------------------------ the products
+      const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
+      const uint32_t idesc_o = idesc_f16(1u, 1u, (uint32_t)kRows, (uint32_t)kHalf);
+      const uint64_t qd = sw128_desc(smem_u32(q_s), 16, 1024);
+      const uint64_t xd = sw128_desc(smem_u32(x_st), 16, 1024), yd = sw128_desc(smem_u32(y_st), 16, 1024);
+      const uint32_t d_s = tmem + TM_S, a_q = tmem + TM_Q, d_o = tmem + TM_O;
+      int gi = 0, ui = 0;
+      bool ok = true;
+      // P V of CTA step g: the own page, then the other
+      auto issue_pv = [&](int g, bool first) -> bool {
+        if (!cluster_wait(p_full, g & 1, p.err, abort_flag)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t pd = noswz_desc(smem_u32(smem + OFF_P + v * P_BYTES), 128, 1024);
+        const uint64_t vd = sw128_desc(smem_u32(v_stage(2 * g)), K_CHUNK, 1024);
+        if (elect_one()) {
+          if (first)
+            umma_ss<0>(d_o, pd, vd, idesc_o);
+          else
+            umma_ss<1>(d_o, pd, vd, idesc_o);
+          umma_ss<1>(d_o, pd + 16, vd + 128, idesc_o);
+          umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
+          umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
+          mma_commit(&v_empty[2 * g % kVStages]);
+        }
+        __syncwarp();
+        if (!warp_wait(&vp_full[g & 1], (g / 2) & 1, p.err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t pd2 = noswz_desc(smem_u32(smem + OFF_P + (v ^ 1u) * P_BYTES), 128, 1024);
+        const uint64_t vd2 = sw128_desc(smem_u32(v_stage(2 * g + 1)), K_CHUNK, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma_ss<1>(d_o, pd2 + 16 * i, vd2 + 128 * i, idesc_o);
+          mma_commit(&v_empty[(2 * g + 1) % kVStages]);
+          mma_commit_both(pv_done);
+        }
+        __syncwarp();
+        return true;
+      };
+      Unit x;
+      for (; ok && take_unit(ui, x);) {
+        const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+        if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
+        ++ui;
+        for (int j = 0; j < nsteps; ++j, ++gi) {
+          if (!(ok = warp_wait(&xy_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
+          if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
+          tc_fence_after();
+          const uint64_t vd = sw128_desc(smem_u32(v_stage(2 * gi)), 16, 1024);
+          constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4 * (kXBlocks + kYBlocks); ++i) {
+              const int c = i >> 2;
+              const uint64_t bd = (c < kXBlocks ? xd + (uint64_t)c * kc : yd + (uint64_t)(c - kXBlocks) * kc) + (uint64_t)(i & 3) * 2;
+              if (i == 0)
+                umma_ss<0>(d_s, qd, bd, idesc_s);
+              else if (c < kSmemQ)
+                umma_ss<1>(d_s, qd + (uint64_t)c * qc + (uint64_t)(i & 3) * 2, bd, idesc_s);
+              else
+                umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), bd, idesc_s);
+              if (i == 4 * kXBlocks - 1) mma_commit(x_empty);
+            }
+            mma_commit(y_empty);
+          }
+          __syncwarp();
+          if (!(ok = warp_wait(&vo_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 4 * (kXBlocks + kYBlocks); i < 4 * kChunks; ++i)
+              umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), vd + (uint64_t)((i >> 2) - kXBlocks - kYBlocks) * kc + (uint64_t)(i & 3) * 2, idesc_s);
+            mma_commit(s_full);
+            if (j == nsteps - 1) mma_commit(q_empty);
+          }
+          __syncwarp();
+          if (j > 0 && !(ok = issue_pv(gi - 1, j == 1))) break;
+        }
+        if (ok) ok = issue_pv(gi - 1, nsteps == 1);
+      }
+      if (elect_one()) mma_commit(fin);
+      __syncwarp();
+      mbar_wait(fin, 0, p.err, nullptr);
+    } else if (warp == kLookupWarp) {
+      // ------------------------------------------------------------------ units and pages, steps ahead
+      int gi = 0;
+      bool ok = true;
+      int u = blockIdx.x / 2, nm = 0;
+      for (int k = 0; ok; ++k) {
+        Unit x;
+        x.rows = -1;
+        if (!p.next || k == 0) {  // both CTAs find it alike
+          for (; u < units; u += clusters) {
+            x = get_unit<kPagesBf16>(p, 2 * u + (int)v, lane == 0 && v == 0 ? p.err : nullptr);
+            if (x.rows > 0) break;
+            x.rows = -1;
+            if (p.next) break;
+          }
+        }
+        if (p.next && x.rows < 0) {  // the next one nobody has: CTA 0 finds it and says so
+          if (v == 0) {
+            while (true) {
+              int n = 0;
+              if (lane == 0) n = clusters + atomicAdd(p.next, 1);
+              u = __shfl_sync(0xFFFFFFFFu, n, 0);
+              if (u >= units) break;
+              x = get_unit<kPagesBf16>(p, 2 * u, lane == 0 ? p.err : nullptr);
+              if (x.rows > 0) break;
+            }
+            if (u >= units) x.rows = -1;
+            if (lane == 0) st_async4(peer_address(smem + OFF_MAIL + (nm % 4) * 4, 1), (uint32_t)u, peer_address(&mail[nm % 4], 1));
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(&mail[nm % 4], 4);
+            __syncwarp();
+            if (!(ok = cluster_wait(&mail[nm % 4], (nm / 4) & 1, p.err, abort_flag))) break;
+            u = *reinterpret_cast<volatile int*>(smem + OFF_MAIL + (nm % 4) * 4);
+            if (u < units) x = get_unit<kPagesBf16>(p, 2 * u + 1, nullptr);
+          }
+          ++nm;
+        }
+        if (k >= kUnitSlots && !(ok = warp_wait(&u_empty[k % kUnitSlots], ((k / kUnitSlots) - 1) & 1, p.err, abort_flag))) break;
+        if (lane == 0) {
+          unit_ring[k % kUnitSlots] = x;
+          mbar_arrive(&u_full[k % kUnitSlots]);
+        }
+        if (x.rows < 0) break;
+        const int32_t* table = p.block_table + (int64_t)x.req * p.max_blocks;
+        const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+        for (int j = 0; j < nsteps; ++j, ++gi) {
+          int page[2];
+          uint32_t may[2][2];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {  // own page, the other
+            const int base = x.lo + (2 * j + (w ? 1 - (int)v : (int)v)) * kTile, lblk = base / kTile;
+            page[w] = -1;
+            may[w][0] = may[w][1] = ~0u;
+            if (base >= x.hi) continue;
+            page[w] = lblk < p.max_blocks ? table[lblk] : -1;
+            if (page[w] < 0 || page[w] >= p.num_blocks) {
+              raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+              page[w] = -1;
+            }
+            if (p.linear_pages && page[w] >= 0) {
+              page[w] = x.req * p.linear_pages + lblk;
+              const uint8_t* f = p.row_ok + (int64_t)page[w] * kTile;
+              may[w][0] = __ballot_sync(0xFFFFFFFFu, f[lane] != 0);
+              may[w][1] = __ballot_sync(0xFFFFFFFFu, f[lane + 32] != 0);
+            }
+          }
+          if (gi >= kSlots && !(ok = warp_wait(&r_empty[gi % kSlots], ((gi / kSlots) - 1) & 1, p.err, abort_flag))) break;
+          if (lane == 0) {
+            int4* e = reinterpret_cast<int4*>(row_ring + gi % kSlots * 8);
+            e[0] = make_int4(page[0], page[1], (int)may[0][0], (int)may[0][1]);
+            e[1] = make_int4((int)may[1][0], (int)may[1][1], 0, 0);
+            mbar_arrive(&r_full[gi % kSlots]);
+          }
+        }
+        if (!ok) break;
+        u += clusters;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // nothing of the other CTA is on its way here any more
+  if (warp == kIssueWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TM_COLS);
+  }
+}
+
+}  // namespace
+
+cudaError_t packed::launch_pair(const Params& p, const CUtensorMap& qmap, const CUtensorMap& rmap, const CUtensorMap& pmap, int num_sms,
+                                cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(mla_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  const int units = p.tiles * p.nsplit, pairs = num_sms / 2;
+  cudaLaunchAttribute attrs[2];
+  const cudaLaunchConfig_t cfg = launch_config(dim3(2 * (units < pairs ? units : pairs)), dim3(kThreads), SMEM, s, attrs, 2);
+  return cudaLaunchKernelEx(&cfg, mla_pair_kernel, qmap, rmap, pmap, p);
+}
+
+}  // namespace dsa
