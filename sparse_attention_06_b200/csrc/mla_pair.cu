@@ -72,15 +72,37 @@ __device__ __forceinline__ uint32_t peer_address(const void* mine, uint32_t rank
 __device__ __forceinline__ void st_async4(uint32_t dst, uint32_t v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst), "r"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_async16(uint32_t dst, uint4 v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+// `bytes` of this CTA's shared memory into the other's, counted likewise
+__device__ __forceinline__ void copy_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-// warp-collective bounded wait for a phase that bytes from the other CTA complete
+// Warp-collective bounded wait, as warp_wait, for a phase that the other CTA takes part in: it acquires at
+// cluster scope (a fence after a plain wait costs several hundred cycles more).
 __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, err, abort_flag);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  const uint32_t b = smem_u32(bar);
+  bool ok = false;
+  long long t0 = 0;
+  for (uint32_t n = 0; !ok; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(b), "r"(parity)
+        : "memory");
+    ok = done != 0;
+    if (ok) break;
+    if (n == 0) t0 = clock64();
+    if (*abort_flag) break;
+    if (clock64() - t0 > kWaitCycles) {
+      raise_error(err, DSA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      break;
+    }
+  }
   return __all_sync(0xFFFFFFFFu, ok);
 }
 // arrive on `bar` of both CTAs once every product issued so far by this thread has completed
@@ -420,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t peer_x_bar = peer_address(&x_bar[quarter], v ^ 1u), peer_p_full = peer_address(p_full, v ^ 1u);
-    uint8_t* p_row = smem + OFF_P + v * P_BYTES + (r >> 3) * 1024 + (r & 7) * 16;
-    const uint32_t peer_p_row = peer_address(p_row, v ^ 1u);
+    uint8_t* p_mine = smem + OFF_P + v * P_BYTES + quarter * 4096;  // P of this warp's rows
+    uint8_t* p_row = p_mine + (lane >> 3) * 1024 + (lane & 7) * 16;
+    const uint32_t peer_p = peer_address(p_mine, v ^ 1u);
     const uint32_t peer_slot = peer_address(smem + OFF_MAX + r * 4, v ^ 1u);
     int gi = 0, nx = 0;
     bool ok = true;
@@ -502,11 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O and both CTAs' P buffers are free once the previous step's P V has completed in both
         if (gi >= 1 && !(ok = cluster_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
 #pragma unroll
-        for (int kc = 0; kc < 8; ++kc) {
-          const uint4 y = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
-          st_async16(peer_p_row + kc * 128, y, peer_p_full);
-          *reinterpret_cast<uint4*>(p_row + kc * 128) = y;
-        }
+        for (int kc = 0; kc < 8; ++kc)
+          *reinterpret_cast<uint4*>(p_row + kc * 128) = make_uint4(pk[4 * kc], pk[4 * kc + 1], pk[4 * kc + 2], pk[4 * kc + 3]);
+        // to the other CTA as one 4 KB copy (stores of 16 bytes got through at ~9 bytes a cycle)
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) copy_to_peer(peer_p, p_mine, 4096u, peer_p_full);
         if (rescale && j > 0) {
           tc_fence_after();
 #pragma unroll 1
@@ -522,10 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(p_full, 32 * 128);  // and the other CTA's P of these 32 rows
+        if (lane == 0) mbar_arrive_expect_tx(p_full, 4096u);  // and the other CTA's P of these 32 rows
       }
       if (!ok) break;
       float other;
