@@ -12,8 +12,8 @@
 //
 // Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
 // three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
-// them, and a ring of three V stages (32 KB: four value blocks of a page, needed until its P V is done), used in the
-// order own page of step 0, other page of step 0, own page of step 1, ...
+// them, and V stages (32 KB: four value blocks of a page) until its P V is done: two for the own page, which Q K^T
+// reads a step before P V does, one for the other page.
 //
 // Roles (16 warps): 0-7 copy (TMA: whole pages as 64-row boxes, a page's visible part by gather4) and move Q into
 // tensor memory; 8-11 softmax and epilogue, one row per thread; 12 issues the products; 13 hands out units and looks
@@ -26,7 +26,6 @@ namespace {
 
 using namespace packed;
 
-constexpr int kVStages = 3;
 constexpr int kIssueWarp = kFillWarps + 4, kLookupWarp = kIssueWarp + 1;
 constexpr int kThreads = 32 * 16;
 // registers a thread by warpgroup: 2 x 96 + 184 + 136 = 4 x 128
@@ -38,8 +37,8 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_P = OFF_Q + kSmemQ * Q_CHUNK;            // [2]: of the page of CTA 0, of CTA 1
 constexpr int OFF_Y = OFF_P + 2 * P_BYTES;
 constexpr int OFF_X = OFF_Y + kYBlocks * K_CHUNK;
-constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;
-constexpr int OFF_BAR = OFF_V + kVStages * V_BYTES;
+constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;          // [2] own page, [1] the other
+constexpr int OFF_BAR = OFF_V + 3 * V_BYTES;
 constexpr int NBAR = 48;
 constexpr int kSlots = 4;
 constexpr int OFF_MASK = OFF_BAR + NBAR * 8;               // [slot] keys of the own page with a row to see, a byte per fill warp
@@ -129,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* land_p = bars + 8;      // [2] other page
   uint64_t* x_empty = bars + 10;    // Q K^T is past the X blocks
   uint64_t* y_empty = bars + 11;    // ... past the Y blocks
-  uint64_t* v_empty = bars + 12;    // [kVStages] P V of the stage done
+  uint64_t* vo_empty = bars + 12;   // [2] P V of the own page done
+  uint64_t* vp_empty = bars + 14;   // P V of the other page done
   uint64_t* q_stage = bars + 15;
   uint64_t* q_read = bars + 16;
   uint64_t* q_full = bars + 17;
@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(x_empty, 1);
     mbar_init(y_empty, 1);
-    for (int i = 0; i < kVStages; ++i) mbar_init(&v_empty[i], 1);
+    mbar_init(&vo_empty[0], 1);
+    mbar_init(&vo_empty[1], 1);
+    mbar_init(vp_empty, 1);
     mbar_init(q_stage, 1);
     mbar_init(q_read, kFillWarps);
     mbar_init(q_full, kFillWarps);
@@ -216,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     last = unit_ring[(k + 1) % kUnitSlots].rows < 0;
     return true;
   };
-  auto v_stage = [&](int item) { return smem + OFF_V + item % kVStages * V_BYTES; };
+  auto v_own = [&](int g) { return smem + OFF_V + (g & 1) * V_BYTES; };
+  uint8_t* v_peer = smem + OFF_V + 2 * V_BYTES;
 
   if (warp < kFillWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
@@ -232,13 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
 
       // --- Q of the unit: places 0 .. 2 of the block order to shared memory, the other six through X, the
-      // first two thirds of Y and the two V stages next in turn to tensor memory
-      uint8_t* stage_at[6] = {x_st, y_st, v_stage(2 * gi), v_stage(2 * gi) + Q_CHUNK, v_stage(2 * gi + 1), v_stage(2 * gi + 1) + Q_CHUNK};
-      auto v_free = [&](int item) {
-        return item < kVStages || warp_wait(&v_empty[item % kVStages], ((item / kVStages) - 1) & 1, p.err, abort_flag);
-      };
+      // first two thirds of Y and the own page's two V stages to tensor memory
+      uint8_t* stage_at[6] = {x_st, y_st, v_own(0), v_own(0) + Q_CHUNK, v_own(1), v_own(1) + Q_CHUNK};
+      auto vo_free = [&](int g) { return g < 2 || warp_wait(&vo_empty[g & 1], ((g / 2) - 1) & 1, p.err, abort_flag); };
       if (ui >= 1 && !(ok = warp_wait(q_empty, (ui - 1) & 1, p.err, abort_flag))) break;
-      if (!(ok = v_free(2 * gi)) || !(ok = v_free(2 * gi + 1))) break;
+      if (!(ok = vo_free(gi)) || !(ok = vo_free(gi + 1))) break;
       if (tid == 0) {
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(q_stage, kChunks * Q_CHUNK);
@@ -346,18 +347,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the other page's V of step j (CTA step g)
       Page peer = {0, -1, {0u, 0u}};
       auto copy_peer = [&](int g) -> bool {
-        const int item = 2 * g + 1, s = g & 1;
+        const int s = g & 1;
         const bool whole = is_whole(peer), partly = is_partly(peer);
-        if (!v_free(item)) return false;
+        if (g >= 1 && !warp_wait(vp_empty, (g - 1) & 1, p.err, abort_flag)) return false;
         uint64_t* bar = partly ? &land_p[s] : &vp_full[s];
         if (lane == 0) fence_proxy_async_smem();
         arm(bar, whole, kVBlocks);
         __syncwarp();
-        copy(peer, whole, row_of(peer), 5, 9, v_stage(item), bar);
+        copy(peer, whole, row_of(peer), 5, 9, v_peer, bar);
         if (partly) {
           if (!warp_wait(&land_p[s], nland_p[s] & 1, p.err, abort_flag)) return false;
           ++nland_p[s];
-          for (int c = 0; c < kVBlocks; ++c) scan(peer, v_stage(item) + c * K_CHUNK, true);
+          for (int c = 0; c < kVBlocks; ++c) scan(peer, v_peer + c * K_CHUNK, true);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&vp_full[s]);
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 
       // Order by when the places become free: X and Y of step g while Q K^T of g - 1 runs, then, as P V of g - 2 goes
-      // on, V of the other page of g - 1 and of the own page of g.
+      // on, V of the own page of g and of the other page of g - 1.
       for (int j = 0; j < nsteps; ++j, ++gi) {
         const int s = gi & 1, slot = gi % kSlots;
         if (!(ok = warp_wait(&r_full[slot], (gi / kSlots) & 1, p.err, abort_flag))) break;
@@ -388,19 +389,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         copy(own, whole, row, 0, 2, x_st, xy_bar);
         if (gi >= 1 && !(ok = warp_wait(y_empty, (gi - 1) & 1, p.err, abort_flag))) break;
         copy(own, whole, row, 2, 5, y_st, xy_bar);
-        if (j > 0 && !(ok = copy_peer(gi - 1))) break;
-        peer = next_peer;
-        if (!(ok = v_free(2 * gi))) break;
+        if (!(ok = vo_free(gi))) break;
         if (!partly) arm(vo_bar, whole, kVBlocks);
         __syncwarp();
-        copy(own, whole, row, 5, 9, v_stage(2 * gi), vo_bar);
+        copy(own, whole, row, 5, 9, v_own(gi), vo_bar);
         if (partly) {
           if (!(ok = warp_wait(&land[s], nland[s] & 1, p.err, abort_flag))) break;
           ++nland[s];
           // values that are not finite become zero in the V blocks and their row is noted: the softmax makes
           // the weights of the tokens that see it NaN.  (In X and Y a NaN only reaches logits, of hidden keys masked ones.)
           uint32_t poison = 0u;
-          for (int c = 0; c < kVBlocks; ++c) poison |= scan(own, v_stage(2 * gi) + c * K_CHUNK, true);
+          for (int c = 0; c < kVBlocks; ++c) poison |= scan(own, v_own(gi) + c * K_CHUNK, true);
           poison |= scan(own, x_st + K_CHUNK, false);
           for (int c = 0; c < kYBlocks; ++c) poison |= scan(own, y_st + c * K_CHUNK, false);
           if (lane == 0) poisons[slot * 8 + warp] = (uint8_t)poison;
@@ -411,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&vo_full[s]);
           }
         }
+        if (j > 0 && !(ok = copy_peer(gi - 1))) break;
+        peer = next_peer;
       }
       if (ok) ok = copy_peer(gi - 1);
       bool last;
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t pd = noswz_desc(smem_u32(smem + OFF_P + v * P_BYTES), 128, 1024);
-        const uint64_t vd = sw128_desc(smem_u32(v_stage(2 * g)), K_CHUNK, 1024);
+        const uint64_t vd = sw128_desc(smem_u32(v_own(g)), K_CHUNK, 1024);
         if (elect_one()) {
           if (first)
             umma_ss<0>(d_o, pd, vd, idesc_o);
@@ -602,17 +603,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_ss<1>(d_o, pd + 16, vd + 128, idesc_o);
           umma_ss<1>(d_o, pd + 32, vd + 256, idesc_o);
           umma_ss<1>(d_o, pd + 48, vd + 384, idesc_o);
-          mma_commit(&v_empty[2 * g % kVStages]);
+          mma_commit(&vo_empty[g & 1]);
         }
         __syncwarp();
         if (!warp_wait(&vp_full[g & 1], (g / 2) & 1, p.err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t pd2 = noswz_desc(smem_u32(smem + OFF_P + (v ^ 1u) * P_BYTES), 128, 1024);
-        const uint64_t vd2 = sw128_desc(smem_u32(v_stage(2 * g + 1)), K_CHUNK, 1024);
+        const uint64_t vd2 = sw128_desc(smem_u32(v_peer), K_CHUNK, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) umma_ss<1>(d_o, pd2 + 16 * i, vd2 + 128 * i, idesc_o);
-          mma_commit(&v_empty[(2 * g + 1) % kVStages]);
+          mma_commit(vp_empty);
           mma_commit_both(pv_done);
         }
         __syncwarp();
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&xy_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
           if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
           tc_fence_after();
-          const uint64_t vd = sw128_desc(smem_u32(v_stage(2 * gi)), 16, 1024);
+          const uint64_t vd = sw128_desc(smem_u32(v_own(gi)), 16, 1024);
           constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
           if (elect_one()) {
 #pragma unroll
