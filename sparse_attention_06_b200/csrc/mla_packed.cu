@@ -946,16 +946,7 @@ cudaError_t launch(Params p, const MlaArgs& a, const void* data, int num_blocks,
   }
   const int units = p.tiles * p.nsplit * 2;
   cudaError_t e = cudaSuccess;
-  if constexpr (kSrc == kPagesBf16) {
-    e = launch_pair(p, qmap, rmap, pmap, num_sms, s);
-  } else {
-  auto kernel = mla_packed_kernel<kSrc>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attrs[2];
-  const cudaLaunchConfig_t cfg = launch_config(dim3(units < num_sms ? units : num_sms), dim3(Roles<kSrc>::kThreads), SMEM, s, attrs);
-  e = cudaLaunchKernelEx(&cfg, kernel, qmap, rmap, pmap, p);
-  }
+  e = launch_pair<kSrc>(p, qmap, rmap, pmap, num_sms, s);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   cudaLaunchAttribute cattrs[2];
   const cudaLaunchConfig_t ccfg = launch_config(dim3(p.T, p.H), dim3(128), 0, s, cattrs);
@@ -1067,8 +1058,9 @@ cudaError_t launch_mla_quantised_tc(const MlaArgs& a, int nsplit, int num_sms, c
   p.T = p.tiles = a.batch.num_queries;
   p.H = p.prows = a.H;
   p.k = a.k;
-  p.nsplit = nsplit;
-  p.ks = ((a.k + nsplit - 1) / nsplit + kTile - 1) / kTile * kTile;
+  // whole steps of 128 keys: at most the planned number of splits, whose partials the workspace holds
+  p.ks = ((a.k + nsplit - 1) / nsplit + 2 * kTile - 1) / (2 * kTile) * (2 * kTile);
+  p.nsplit = nsplit > 1 ? (a.k + p.ks - 1) / p.ks : 1;
   p.num_reqs = a.batch.num_reqs;
   p.max_blocks = a.batch.max_blocks;
   p.max_context = a.batch.max_context;

@@ -328,6 +328,7 @@ __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t
 
 // Chunks over bf16 rows on CTA pairs (mla_pair.cu): tensor maps of the queries (128-row boxes), the rows one by one and
 // whole pages.
+template <Source kSrc>
 cudaError_t launch_pair(const Params& p, const CUtensorMap& qmap, const CUtensorMap& rmap, const CUtensorMap& pmap, int num_sms,
                         cudaStream_t s);
 

@@ -28,8 +28,13 @@ using namespace packed;
 
 constexpr int kIssueWarp = kFillWarps + 4, kLookupWarp = kIssueWarp + 1;
 constexpr int kThreads = 32 * 16;
-// registers a thread by warpgroup: 2 x 96 + 184 + 136 = 4 x 128
-constexpr int kFillRegs = 96, kSoftmaxRegs = 184, kIssueRegs = 136;
+// Registers a thread by warpgroup, 4 x 128 in all.  Spilled ones cost more than elsewhere: they miss the small L1
+// left beside 220 KB of shared memory.
+template <Source kSrc>
+struct Regs {
+  static constexpr bool kQuant = kSrc != kPagesBf16;
+  static constexpr int kFill = kQuant ? 168 : 96, kSoftmax = kQuant ? 112 : 184, kIssue = kQuant ? 64 : 136;
+};
 
 constexpr int P_BYTES = kRows * kTile * 2;
 constexpr int V_BYTES = kVBlocks * K_CHUNK;
@@ -46,8 +51,9 @@ constexpr int OFF_POISON = OFF_MASK + kSlots * 8;          // [slot] rows with N
 constexpr int OFF_STATS = OFF_POISON + kSlots * 8;         // 1 / l of each row (last unit)
 constexpr int OFF_MAX = OFF_STATS + kRows * 4;             // [2][128] values of the other CTA's rows
 constexpr int OFF_UNIT = OFF_MAX + 2 * kRows * 4;          // [2] units in hand
-constexpr int OFF_ROWS = OFF_UNIT + kUnitSlots * 40;       // [slot] own page, other page, masks of their rows that may be read
-constexpr int OFF_MAIL = OFF_ROWS + kSlots * 32;           // [4] units from CTA 0
+constexpr int OFF_ROWS = OFF_UNIT + kUnitSlots * 40;       // [slot] bf16: own page, other page, masks of their rows that may be
+                                                           // read; quantised: [2][64] pool row of each key of either, -1: none
+constexpr int OFF_MAIL = OFF_ROWS + kSlots * 2 * kTile * 4;           // [4] units from CTA 0
 constexpr int OFF_MISC = OFF_MAIL + 16;
 constexpr int SMEM = OFF_MISC + 16;
 static_assert(SMEM <= 232448, "shared memory budget");
@@ -112,9 +118,11 @@ __device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
       : "memory");
 }
 
+template <Source kSrc>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
                     const __grid_constant__ CUtensorMap pmap, const Params p) {
+  constexpr bool kQuant = kSrc != kPagesBf16;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t v = cluster_rank();  // this CTA's value half, and its page of each step
   uint8_t* q_s = smem + OFF_Q;
@@ -222,7 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* v_peer = smem + OFF_V + 2 * V_BYTES;
 
   if (warp < kFillWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
+    if constexpr (kQuant)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kFill));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kFill));
     // ------------------------------------------------------------------ copies, and Q into tensor memory
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -233,6 +244,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit x;
     for (; ok && take_unit(ui, x);) {
       const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+
+      // --- Quantised rows in flight.  A warp has eight keys of either page, pair q its keys 2 q + half; a lane has 16
+      // codes of a row: of the own page in the other half of the values (code_o) and in this one (code_v), of the
+      // other page in this half (code_p).  Lane l has the scale of key l / 4, group l % 4.  Loads of one kind
+      // are issued together, a third to two thirds of a step ahead of their use: a warp waits for loads by a handful of counters, so waiting
+      // for an old load can mean waiting for a young one that shares its counter.  None is conditional (a key
+      // without a row reads row 0).
+      const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // eight lanes: four pieces of both rows of a pair
+      uint4 code_o[4], code_v[4], code_p[4];
+      float sc_own = 1.0f, sc_peer = 1.0f;
+      uint32_t seen_own = 0u, bad_own = 0u, none_peer = 0u;  // lanes: key with a row; no row, or a scale that is no power of two; no row
+      auto row_at = [&](int g, int which, int k8) -> int { return row_ring[(g % kSlots * 2 + which) * kTile + warp * kKeysPerWarp + k8]; };
+      auto load_codes = [&](uint4(&code)[4], int g, int which, uint32_t h) {
+        const uint8_t* base = p.data + 256 * h + 16 * l16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) code[q] = load16_here(base + (int64_t)max(0, row_at(g, which, 2 * q + half)) * kLatentBytes);
+      };
+      auto load_scales = [&](int g, int which) -> float {
+        return loadf_here(p.scale + (int64_t)max(0, row_at(g, which, lane >> 2)) * 4 + (lane & 3));
+      };
+      auto check_own = [&](int g) {
+        const bool none = row_at(g, 0, lane >> 2) < 0;
+        bad_own = __ballot_sync(0xFFFFFFFFu, none || !latent_scale_ok(sc_own));
+        seen_own = ~__ballot_sync(0xFFFFFFFFu, none);
+      };
+      // 16 codes of each pair's row, in value half h, into the row's blocks: `dst` is the lane's 64-dim block, pieces
+      // 2 (l16 % 4) and the next; the two rows of a pair differ in bit 0, so eight lanes store to all eight bank groups.
+      // partly: only some of the tile's tokens see the rows, and a NaN must not reach the others through 0 * NaN in
+      // P V: it becomes zero and its row is noted, so that the softmax makes the weights of those that see it NaN
+      // (elsewhere a NaN takes its natural course).
+      auto put_all = [&](const uint4(&code)[4], float sc, uint32_t bad, uint32_t h, bool partly, uint8_t* dst, uint32_t& nan_rows) {
+        auto put = [&](auto plain, int q) {
+          constexpr bool kPlain = decltype(plain)::value;
+          const int k8 = 2 * q + half, r = warp * kKeysPerWarp + k8;
+          uint32_t w[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
+          float my_sc = __shfl_sync(0xFFFFFFFFu, sc, k8 * 4 + 2 * (int)h + (l16 >> 3));
+          if (!kPlain && ((bad >> (4 * k8)) & 0xFu)) {
+            w[0] = w[1] = w[2] = w[3] = 0u;
+            my_sc = 1.0f;
+          }
+          uint32_t b[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) decode4(w[i], make_float2(my_sc, my_sc), b[2 * i], b[2 * i + 1]);
+          if (!kPlain && partly) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if ((b[i] & 0x7F80u) == 0x7F80u) { b[i] &= 0xFFFF0000u; nan_rows |= 1u << k8; }
+              if ((b[i] & 0x7F800000u) == 0x7F800000u) { b[i] &= 0xFFFFu; nan_rows |= 1u << k8; }
+            }
+          }
+          const uint32_t piece = (uint32_t)(l16 & 3) * 2u, x7 = (uint32_t)(r & 7);
+          *reinterpret_cast<uint4*>(dst + r * 128 + ((piece ^ x7) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+          *reinterpret_cast<uint4*>(dst + r * 128 + (((piece + 1u) ^ x7) << 4)) = make_uint4(b[4], b[5], b[6], b[7]);
+        };
+        if (bad == 0u && !partly) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) put(Flag<true>(), q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) put(Flag<false>(), q);
+        }
+      };
+      // the other page's V of step j (CTA step g): its loads (the last look at the step's rows) ...
+      auto load_peer = [&](int g) {
+        sc_peer = load_scales(g, 1);
+        load_codes(code_p, g, 1, v);
+        none_peer = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);
+        if (lane == 0) mbar_arrive(&r_empty[g % kSlots]);
+      };
+      // ... and its codes into place
+      auto put_peer = [&](int g, int j) -> bool {
+        if (g >= 1 && !warp_wait(vp_empty, (g - 1) & 1, p.err, abort_flag)) return false;
+        const int base = x.lo + (2 * j + 1 - (int)v) * kTile;
+        const bool partly = kSrc != kSelected && base + kTile - 1 > x.tok0 && x.hi - 1 > max(x.tok0, base - 1);
+        uint32_t nan_rows = 0u;
+        const uint32_t bad = none_peer | __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc_peer) && ((uint32_t)(lane & 3) >> 1) == v);
+        put_all(code_p, sc_peer, bad, v, partly, v_peer + (l16 >> 2) * K_CHUNK, nan_rows);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vp_full[g & 1]);
+        return true;
+      };
+      if (kQuant && nsteps > 0) {
+        if (!(ok = warp_wait(&r_full[gi % kSlots], (gi / kSlots) & 1, p.err, abort_flag))) break;
+        sc_own = load_scales(gi, 0);
+        load_codes(code_o, gi, 0, v ^ 1u);
+        load_codes(code_v, gi, 0, v);
+        check_own(gi);
+      }
 
       // --- Q of the unit: places 0 .. 2 of the block order to shared memory, the other six through X, the
       // first two thirds of Y and the own page's two V stages to tensor memory
@@ -275,6 +375,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = warp_wait(q_read, ui & 1, p.err, abort_flag))) break;
       ++ui;
 
+      if constexpr (kQuant) {
+        for (int j = 0; j < nsteps; ++j, ++gi) {
+          const int s = gi & 1, slot = gi % kSlots;
+          const bool more = j + 1 < nsteps;
+          const bool partly = kSrc != kSelected && x.lo + (2 * j + (int)v + 1) * kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
+          uint32_t nan_rows = 0u;
+          const uint32_t bad = bad_own;
+          // X1 and Y: the own page's values of the other half; X0: its RoPE part as it is, in the background
+          if (gi >= 1 && (!(ok = warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag)) || !(ok = warp_wait(y_empty, (gi - 1) & 1, p.err, abort_flag)))) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r8 = 4 * i + (lane >> 3);
+            const int r = warp * kKeysPerWarp + r8;
+            cp_async_16(smem_u32(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
+                        p.data + (int64_t)max(0, row_at(gi, 0, r8)) * kLatentBytes + kDv + 16 * (lane & 7),
+                        ((bad >> (4 * r8)) & 0xFu) ? 0u : 16u);
+          }
+          put_all(code_o, sc_own, bad, v ^ 1u, partly, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK, nan_rows);
+          if (j > 0) load_peer(gi - 1);
+          // V: its values of this half
+          if (!(ok = vo_free(gi))) break;
+          put_all(code_v, sc_own, bad, v, partly, v_own(gi) + (l16 >> 2) * K_CHUNK, nan_rows);
+          float sc_next = 1.0f;
+          if (more) {
+            if (!(ok = warp_wait(&r_full[(gi + 1) % kSlots], ((gi + 1) / kSlots) & 1, p.err, abort_flag))) break;
+            sc_next = load_scales(gi + 1, 0);
+            load_codes(code_o, gi + 1, 0, v ^ 1u);
+          }
+          const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
+          if (lane == 0) {
+            uint32_t valid = 0xFFu;
+            if (bad) {
+              bool flag = false;
+              for (int r8 = 0; r8 < kKeysPerWarp; ++r8)
+                if ((bad >> (4 * r8)) & 0xFu) {
+                  valid &= ~(1u << r8);
+                  flag |= (seen_own >> (4 * r8)) & 1u;
+                }
+              if (flag) raise_error(p.err, DSA_DEVERR_SCALE);
+            }
+            masks[slot * 8 + warp] = (uint8_t)valid;
+            poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
+          }
+          cp_async_wait_all();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&xy_full[s]);
+            mbar_arrive(&vo_full[s]);
+          }
+          // V of the other page, a step behind
+          if (j > 0 && !(ok = put_peer(gi - 1, j - 1))) break;
+          if (more) {
+            load_codes(code_v, gi + 1, 0, v);
+            sc_own = sc_next;
+            check_own(gi + 1);
+          }
+        }
+        if (ok && nsteps > 0) {
+          load_peer(gi - 1);
+          ok = put_peer(gi - 1, nsteps - 1);
+        }
+      } else {
       // --- copies.  A page: its first position, its number (-1: none), its rows that may be read.
       struct Page {
         int base, page;
@@ -414,18 +577,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         peer = next_peer;
       }
       if (ok) ok = copy_peer(gi - 1);
+      }
       bool last;
       if (!ok || !(ok = last_unit(ui - 1, last))) break;
       if (last) {
         if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
         tc_fence_after();
-        store_o(p, x, my_lanes, quarter, 64 + 96 * part, 160 + 96 * part, smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], true);
+        store_o(p, x, my_lanes, quarter, 64 + 96 * part, 160 + 96 * part, smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], nsteps > 0);
         tc_fence_before();
       }
     }
     // gave up: copies in flight must land before the CTA exits
     if (!ok && staged) mbar_wait(q_stage, ui & 1, p.err, nullptr);
-    if (!ok && lane == 0) {
+    if (!ok && !kQuant && lane == 0) {
       for (int t = gi > 0 ? gi - 1 : 0; t <= gi; ++t) {
         mbar_wait(&xy_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr, kWaitCycles / 16);
         mbar_wait(&vo_full[t & 1], (uint32_t)((t / 2) & 1), p.err, nullptr, kWaitCycles / 16);
@@ -437,7 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kIssueWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if constexpr (kQuant)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kSoftmax));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kSoftmax));
     // ------------------------------------------------------------------ softmax and epilogue
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
@@ -464,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit x;
     for (int ui = 0; ok && take_unit(ui, x); ++ui) {
       const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
-      const int limit = r < x.rows ? x.tok0 + (x.h0 + r) / p.H : -1;  // last position this row sees
+      // last position this row sees (kSelected: the keys' own mask tells)
+      const int limit = r >= x.rows ? -1 : kSrc == kSelected ? 0x7FFFFFFF : x.tok0 + (x.h0 + r) / p.H;
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < nsteps; ++j, ++gi) {
         const int slot = gi % kSlots;
@@ -555,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float other;
       if (!(ok = exchange(l, other))) break;
       l = v ? other + l : l + other;
-      if (!(ok = cluster_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
+      if (nsteps > 0 && !(ok = cluster_wait(pv_done, (gi - 1) & 1, p.err, abort_flag))) break;
       tc_fence_after();
       // a row that saw nothing: 0 and -inf; NaN stays NaN
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -567,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ep_last);
       }
-      store_o(p, x, lane_base, quarter, 0, last ? 64 : kHalf, smem + OFF_P + v * P_BYTES + quarter * 2048, inv, true);
+      store_o(p, x, lane_base, quarter, 0, last ? 64 : kHalf, smem + OFF_P + v * P_BYTES + quarter * 2048, inv, nsteps > 0);
       if (v == 0 && r < x.rows) {
         if (x.splits == 1) {
           if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;
@@ -578,7 +746,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if constexpr (kQuant)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kIssue));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kIssue));
     if (warp == kIssueWarp) {
       // ------------------------------------------------------------------ the products
       const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
@@ -624,14 +795,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
         if (!(ok = warp_wait(q_full, ui & 1, p.err, abort_flag))) break;
         ++ui;
+        if (nsteps == 0) {
+          if (elect_one()) mma_commit(q_empty);
+          __syncwarp();
+        }
         for (int j = 0; j < nsteps; ++j, ++gi) {
           if (!(ok = warp_wait(&xy_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
           if (gi >= 1 && !(ok = warp_wait(s_empty, (gi - 1) & 1, p.err, abort_flag))) break;
           tc_fence_after();
           const uint64_t vd = sw128_desc(smem_u32(v_own(gi)), 16, 1024);
           constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
+          // (unrolled the products go out a third faster; quantised rows are slower still, and want the registers)
+          constexpr int kUnroll = kQuant ? 4 : 64;
           if (elect_one()) {
-#pragma unroll
+#pragma unroll kUnroll
             for (int i = 0; i < 4 * (kXBlocks + kYBlocks); ++i) {
               const int c = i >> 2;
               const uint64_t bd = (c < kXBlocks ? xd + (uint64_t)c * kc : yd + (uint64_t)(c - kXBlocks) * kc) + (uint64_t)(i & 3) * 2;
@@ -649,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&vo_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
+#pragma unroll kUnroll
             for (int i = 4 * (kXBlocks + kYBlocks); i < 4 * kChunks; ++i)
               umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), vd + (uint64_t)((i >> 2) - kXBlocks - kYBlocks) * kc + (uint64_t)(i & 3) * 2, idesc_s);
             mma_commit(s_full);
@@ -658,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (j > 0 && !(ok = issue_pv(gi - 1, j == 1))) break;
         }
-        if (ok) ok = issue_pv(gi - 1, nsteps == 1);
+        if (ok && nsteps > 0) ok = issue_pv(gi - 1, nsteps == 1);
       }
       if (elect_one()) mma_commit(fin);
       __syncwarp();
@@ -673,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.rows = -1;
         if (!p.next || k == 0) {  // both CTAs find it alike
           for (; u < units; u += clusters) {
-            x = get_unit<kPagesBf16>(p, 2 * u + (int)v, lane == 0 && v == 0 ? p.err : nullptr);
+            x = get_unit<kSrc>(p, 2 * u + (int)v, lane == 0 && v == 0 ? p.err : nullptr);
             if (x.rows > 0) break;
             x.rows = -1;
             if (p.next) break;
@@ -686,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) n = clusters + atomicAdd(p.next, 1);
               u = __shfl_sync(0xFFFFFFFFu, n, 0);
               if (u >= units) break;
-              x = get_unit<kPagesBf16>(p, 2 * u, lane == 0 ? p.err : nullptr);
+              x = get_unit<kSrc>(p, 2 * u, lane == 0 ? p.err : nullptr);
               if (x.rows > 0) break;
             }
             if (u >= units) x.rows = -1;
@@ -696,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!(ok = cluster_wait(&mail[nm % 4], (nm / 4) & 1, p.err, abort_flag))) break;
             u = *reinterpret_cast<volatile int*>(smem + OFF_MAIL + (nm % 4) * 4);
-            if (u < units) x = get_unit<kPagesBf16>(p, 2 * u + 1, nullptr);
+            if (u < units) x = get_unit<kSrc>(p, 2 * u + 1, nullptr);
           }
           ++nm;
         }
@@ -706,8 +883,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&u_full[k % kUnitSlots]);
         }
         if (x.rows < 0) break;
-        const int32_t* table = p.block_table + (int64_t)x.req * p.max_blocks;
+        const int32_t* table = p.block_table + (int64_t)max(0, x.req) * p.max_blocks;
         const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
+        if constexpr (kQuant) {
+          // lane: keys lane and lane + 32 of the own page and of the other; selected positions are loaded a step ahead
+          auto position = [&](int j, int e) -> int {
+            const int slot = x.lo + (2 * j + (e < 2 ? (int)v : 1 - (int)v)) * kTile + lane + 32 * (e & 1);
+            if (slot >= x.hi) return -1;
+            return kSrc == kSelected && p.idx ? p.idx[(int64_t)(x.row0 / p.H) * p.k + slot] : slot;
+          };
+          int ps[4], next[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ps[e] = position(0, e);
+          for (int j = 0; j < nsteps; ++j, ++gi) {
+            int row[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) next[e] = position(j + 1, e);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool seen = x.req >= 0 && ps[e] >= 0 && (kSrc != kSelected || ps[e] <= x.tok0);
+              row[e] = seen && ps[e] / kTile < p.max_blocks ? table[ps[e] / kTile] : -1;
+              if (seen && (row[e] < 0 || row[e] >= p.num_blocks)) {
+                if (e < 2) raise_error(p.err, DSA_DEVERR_BLOCK_ID);
+                row[e] = -1;
+              }
+              if (row[e] >= 0) row[e] = row[e] * kTile + ps[e] % kTile;
+              if (kSrc == kSelected && e < 2 && !seen && ps[e] != -1 && x.req >= 0) raise_error(p.err, DSA_DEVERR_INDEX);
+            }
+            if (gi >= kSlots && !(ok = warp_wait(&r_empty[gi % kSlots], ((gi / kSlots) - 1) & 1, p.err, abort_flag))) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) row_ring[(gi % kSlots * 2 + (e >> 1)) * kTile + lane + 32 * (e & 1)] = row[e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&r_full[gi % kSlots]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ps[e] = next[e];
+          }
+        } else
         for (int j = 0; j < nsteps; ++j, ++gi) {
           int page[2];
           uint32_t may[2][2];
@@ -755,14 +966,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+template <Source kSrc>
 cudaError_t packed::launch_pair(const Params& p, const CUtensorMap& qmap, const CUtensorMap& rmap, const CUtensorMap& pmap, int num_sms,
                                 cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(mla_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  auto kernel = mla_pair_kernel<kSrc>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const int units = p.tiles * p.nsplit, pairs = num_sms / 2;
   cudaLaunchAttribute attrs[2];
   const cudaLaunchConfig_t cfg = launch_config(dim3(2 * (units < pairs ? units : pairs)), dim3(kThreads), SMEM, s, attrs, 2);
-  return cudaLaunchKernelEx(&cfg, mla_pair_kernel, qmap, rmap, pmap, p);
+  return cudaLaunchKernelEx(&cfg, kernel, qmap, rmap, pmap, p);
 }
+template cudaError_t packed::launch_pair<kSelected>(const Params&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+template cudaError_t packed::launch_pair<kPages>(const Params&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+template cudaError_t packed::launch_pair<kPagesBf16>(const Params&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 
 }  // namespace dsa
