@@ -94,11 +94,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 
-// Loads that stay where they are written: left to itself the compiler moves the loads of the next tile down to
-// their use, a tile later, and with them their whole latency.
+// Loads that stay where they are written: left to itself the compiler moves loads for later down to their use, and
+// with them their whole latency.
 __device__ __forceinline__ uint4 load16_here(const void* a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
   return v;
 }
 __device__ __forceinline__ float loadf_here(const float* a) {

@@ -1,24 +1,42 @@
-// mla_pair.cu -- dense MLA (MQA mode) of chunks of new tokens over bf16 rows, a CTA pair to a tile of 128
-// query rows (mla_packed.cu has the packing of query rows, and the quantised sources).
+// mla_pair.cu -- MLA (MQA mode) for tiles of 128 query rows on tcgen05 tensor cores, a CTA pair to a tile: dense
+// attention of chunks over the paged latent cache, and sparse attention over quantised latents.
 //
-// O of 128 rows x 512 values in f32 fills tensor memory, so the values are split over two CTAs; if each computed
-// S = Q K^T for itself, 576 of 1088 multiplications would be done twice.  Here the two are a cluster: of every
-// 128 keys (a step) each computes S and P for its own 64-key page, and hands P to the other through distributed
-// shared memory (16 KB a step); both multiply the whole P (128 rows x 128 keys) with their half of the values.
-// Softmax bases have to agree: the rows' maxima of the two pages are exchanged first (one f32 a row).
+// Mathematics: out = softmax(tau Q K^T + mask) V with K the 576-wide latent rows and V their first 512 elements, by
+// one pass over the keys with a running maximum and sum per query row.
+//
+// Query rows.  A token's H heads are H rows of the [num_tokens * H, 576] query matrix and a chunk's tokens follow each
+// other, so 128 consecutive rows of that matrix are one tensor-core tile whatever H is: with 16 heads a tile holds
+// eight tokens of the request, which share every key.  The causal mask is the only thing that differs between the tokens
+// of a tile.  (Sparse attention: one query per tile, its keys are its own.)
+//
+// The pair.  O of 128 rows x 512 values in f32 fills tensor memory, so the values are split over two CTAs; if each
+// computed S = Q K^T for itself, 576 of 1088 multiplications would be done twice (measured: 1.48 ms for 512 tokens x
+// 64 heads at 16k context, against 1.15 ms).  Here the two are a cluster: of every 128 keys (a step) each computes S and
+// P for its own 64-key page, and copies P to the other through distributed shared memory (16 KB a step); both multiply
+// the whole P (128 rows x 128 keys) with their half of the values.  Softmax bases have to agree: the rows' maxima of the
+// two pages are exchanged first (one f32 a row).
 //
 // Per step and CTA: Q K^T of 64 keys (36 products of N = 64, ~1340 cycles), P V of 128 keys (8 of N = 256, 1024), into
 // shared memory the own page's nine 64-dim column blocks (72 KB) and this half's four of the other page (32 KB).
+// What bounds it: over bf16 rows the shared-memory port (~2800 of ~3500 cycles a step: the copies in, the products'
+// operands, P); over quantised rows the warps that turn codes into bf16 (~6500 cycles a step).
 //
 // Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
 // three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
 // them, and V stages (32 KB: four value blocks of a page) until its P V is done: two for the own page, which Q K^T
-// reads a step before P V does, one for the other page.
+// reads a step before P V does, one for the other page.  Blocks are 64 rows x 64 dims, 128B-swizzled: the same bytes
+// are the K-major B of Q K^T and the MN-major B of P V.
 //
-// Roles (16 warps): 0-7 copy (TMA: whole pages as 64-row boxes, a page's visible part by gather4) and move Q into
-// tensor memory; 8-11 softmax and epilogue, one row per thread; 12 issues the products; 13 hands out units and looks
-// pages up.  Order of products: Q K^T of step g, then P V of step g - 1, so that the tensor core has P V to do while the
-// softmax reads S.  All waits are bounded; bad rows set the device error word and are skipped.
+// Quantised rows become bf16 on their way in: eight warps load a row's codes with 16-byte loads, turn them into bf16
+// (exact: a code has four significant bits and its scale is a power of two) and store them in the swizzled layout; the
+// other page's half is converted again rather than copied (its place is free only when X and Y are wanted for the next
+// step).  bf16 rows come by TMA: whole 64-token pages as 64-row boxes, a page's visible part by gather4.
+//
+// Roles (16 warps): 0-7 fill the blocks and move Q into tensor memory; 8-11 softmax and epilogue, one row per thread;
+// 12 issues the products (the whole warp, so that the compiler keeps the issue uniform: with elect.sync one product of
+// N = 64 goes out every ~32 cycles, against ~60 from a thread chosen by its index); 13 hands out units and looks pages
+// up, steps ahead.  Order of products: Q K^T of step g, then P V of step g - 1, so that the tensor core has P V to do
+// while the softmax reads S.  All waits are bounded; bad rows set the device error word and are skipped.
 #include "mla_packed.cuh"
 
 namespace dsa {
@@ -29,12 +47,19 @@ using namespace packed;
 constexpr int kIssueWarp = kFillWarps + 4, kLookupWarp = kIssueWarp + 1;
 constexpr int kThreads = 32 * 16;
 // Registers a thread by warpgroup, 4 x 128 in all.  Spilled ones cost more than elsewhere: they miss the small L1
-// left beside 220 KB of shared memory.
+// left beside 220 KB of shared memory (300 bytes of spill loads in the quantised fill: 1.06 -> 1.17 ms for a prefill of
+// 1024 queries).
 template <Source kSrc>
 struct Regs {
   static constexpr bool kQuant = kSrc != kPagesBf16;
-  static constexpr int kFill = kQuant ? 168 : 96, kSoftmax = kQuant ? 112 : 184, kIssue = kQuant ? 64 : 136;
+  static constexpr int kFill = kQuant ? 136 : 96, kSoftmax = kQuant ? 128 : 184, kIssue = kQuant ? 112 : 136;
 };
+
+template <int kRegs>
+__device__ __forceinline__ void set_registers() {  // of this warp's warpgroup; 128 at launch
+  if constexpr (kRegs > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  if constexpr (kRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 constexpr int P_BYTES = kRows * kTile * 2;
 constexpr int V_BYTES = kVBlocks * K_CHUNK;
@@ -230,10 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* v_peer = smem + OFF_V + 2 * V_BYTES;
 
   if (warp < kFillWarps) {
-    if constexpr (kQuant)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kFill));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kFill));
+    set_registers<Regs<kSrc>::kFill>();
     // ------------------------------------------------------------------ copies, and Q into tensor memory
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -245,21 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && take_unit(ui, x);) {
       const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
 
-      // --- Quantised rows in flight.  A warp has eight keys of either page, pair q its keys 2 q + half; a lane has 16
-      // codes of a row: of the own page in the other half of the values (code_o) and in this one (code_v), of the
-      // other page in this half (code_p).  Lane l has the scale of key l / 4, group l % 4.  Loads of one kind
-      // are issued together, a third to two thirds of a step ahead of their use: a warp waits for loads by a handful of counters, so waiting
-      // for an old load can mean waiting for a young one that shares its counter.  None is conditional (a key
-      // without a row reads row 0).
+      // --- Quantised rows.  A warp has eight keys of either page, pair q its keys 2 q + half; a lane has 16 codes of a
+      // row in one half of the values.  Lane l has the scale of key l / 4, group l % 4.  Codes are fetched into L1 one or
+      // two conversions ahead of their load (in registers they would be 48 more, and loads in flight share the few
+      // counters a warp waits by).  A key without a row reads row 0.
       const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // eight lanes: four pieces of both rows of a pair
-      uint4 code_o[4], code_v[4], code_p[4];
+      uint4 code[4];
       float sc_own = 1.0f, sc_peer = 1.0f;
       uint32_t seen_own = 0u, bad_own = 0u, none_peer = 0u;  // lanes: key with a row; no row, or a scale that is no power of two; no row
       auto row_at = [&](int g, int which, int k8) -> int { return row_ring[(g % kSlots * 2 + which) * kTile + warp * kKeysPerWarp + k8]; };
-      auto load_codes = [&](uint4(&code)[4], int g, int which, uint32_t h) {
+      auto load_codes = [&](int g, int which, uint32_t h) {
         const uint8_t* base = p.data + 256 * h + 16 * l16;
 #pragma unroll
         for (int q = 0; q < 4; ++q) code[q] = load16_here(base + (int64_t)max(0, row_at(g, which, 2 * q + half)) * kLatentBytes);
+      };
+      auto fetch = [&](int g, int which, uint32_t h) {
+        const uint8_t* a = p.data + (int64_t)max(0, row_at(g, which, lane >> 2)) * kLatentBytes + 256 * h + 64 * (lane & 3);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a));  // (a row's 256 bytes: four lanes)
       };
       auto load_scales = [&](int g, int which) -> float {
         return loadf_here(p.scale + (int64_t)max(0, row_at(g, which, lane >> 2)) * 4 + (lane & 3));
@@ -269,12 +293,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad_own = __ballot_sync(0xFFFFFFFFu, none || !latent_scale_ok(sc_own));
         seen_own = ~__ballot_sync(0xFFFFFFFFu, none);
       };
-      // 16 codes of each pair's row, in value half h, into the row's blocks: `dst` is the lane's 64-dim block, pieces
+      // The 16 codes of each pair's row in `code`, of value half h, into the row's blocks: `dst` is the lane's 64-dim block, pieces
       // 2 (l16 % 4) and the next; the two rows of a pair differ in bit 0, so eight lanes store to all eight bank groups.
       // partly: only some of the tile's tokens see the rows, and a NaN must not reach the others through 0 * NaN in
       // P V: it becomes zero and its row is noted, so that the softmax makes the weights of those that see it NaN
       // (elsewhere a NaN takes its natural course).
-      auto put_all = [&](const uint4(&code)[4], float sc, uint32_t bad, uint32_t h, bool partly, uint8_t* dst, uint32_t& nan_rows) {
+      auto put_all = [&](float sc, uint32_t bad, uint32_t h, bool partly, uint8_t* dst, uint32_t& nan_rows) {
         auto put = [&](auto plain, int q) {
           constexpr bool kPlain = decltype(plain)::value;
           const int k8 = 2 * q + half, r = warp * kKeysPerWarp + k8;
@@ -306,12 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) put(Flag<false>(), q);
         }
       };
-      // the other page's V of step j (CTA step g): its loads (the last look at the step's rows) ...
-      auto load_peer = [&](int g) {
+      // the other page's V of step j (CTA step g): on its way ...
+      auto fetch_peer = [&](int g) {
         sc_peer = load_scales(g, 1);
-        load_codes(code_p, g, 1, v);
+        fetch(g, 1, v);
         none_peer = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);
-        if (lane == 0) mbar_arrive(&r_empty[g % kSlots]);
       };
       // ... and its codes into place
       auto put_peer = [&](int g, int j) -> bool {
@@ -319,8 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int base = x.lo + (2 * j + 1 - (int)v) * kTile;
         const bool partly = kSrc != kSelected && base + kTile - 1 > x.tok0 && x.hi - 1 > max(x.tok0, base - 1);
         uint32_t nan_rows = 0u;
+        load_codes(g, 1, v);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&r_empty[g % kSlots]);
         const uint32_t bad = none_peer | __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc_peer) && ((uint32_t)(lane & 3) >> 1) == v);
-        put_all(code_p, sc_peer, bad, v, partly, v_peer + (l16 >> 2) * K_CHUNK, nan_rows);
+        put_all(sc_peer, bad, v, partly, v_peer + (l16 >> 2) * K_CHUNK, nan_rows);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&vp_full[g & 1]);
@@ -329,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kQuant && nsteps > 0) {
         if (!(ok = warp_wait(&r_full[gi % kSlots], (gi / kSlots) & 1, p.err, abort_flag))) break;
         sc_own = load_scales(gi, 0);
-        load_codes(code_o, gi, 0, v ^ 1u);
-        load_codes(code_v, gi, 0, v);
+        fetch(gi, 0, v ^ 1u);
+        fetch(gi, 0, v);
         check_own(gi);
       }
 
@@ -392,16 +418,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p.data + (int64_t)max(0, row_at(gi, 0, r8)) * kLatentBytes + kDv + 16 * (lane & 7),
                         ((bad >> (4 * r8)) & 0xFu) ? 0u : 16u);
           }
-          put_all(code_o, sc_own, bad, v ^ 1u, partly, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK, nan_rows);
-          if (j > 0) load_peer(gi - 1);
+          load_codes(gi, 0, v ^ 1u);
+          put_all(sc_own, bad, v ^ 1u, partly, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK, nan_rows);
+          if (j > 0) fetch_peer(gi - 1);
           // V: its values of this half
           if (!(ok = vo_free(gi))) break;
-          put_all(code_v, sc_own, bad, v, partly, v_own(gi) + (l16 >> 2) * K_CHUNK, nan_rows);
+          load_codes(gi, 0, v);
+          put_all(sc_own, bad, v, partly, v_own(gi) + (l16 >> 2) * K_CHUNK, nan_rows);
           float sc_next = 1.0f;
           if (more) {
             if (!(ok = warp_wait(&r_full[(gi + 1) % kSlots], ((gi + 1) / kSlots) & 1, p.err, abort_flag))) break;
             sc_next = load_scales(gi + 1, 0);
-            load_codes(code_o, gi + 1, 0, v ^ 1u);
+            fetch(gi + 1, 0, v ^ 1u);
           }
           const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
           if (lane == 0) {
@@ -428,13 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V of the other page, a step behind
           if (j > 0 && !(ok = put_peer(gi - 1, j - 1))) break;
           if (more) {
-            load_codes(code_v, gi + 1, 0, v);
+            fetch(gi + 1, 0, v);
             sc_own = sc_next;
             check_own(gi + 1);
           }
         }
         if (ok && nsteps > 0) {
-          load_peer(gi - 1);
+          fetch_peer(gi - 1);
           ok = put_peer(gi - 1, nsteps - 1);
         }
       } else {
@@ -601,10 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kIssueWarp) {
-    if constexpr (kQuant)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kSoftmax));
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kSoftmax));
+    set_registers<Regs<kSrc>::kSoftmax>();
     // ------------------------------------------------------------------ softmax and epilogue
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
@@ -746,10 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
   } else {
-    if constexpr (kQuant)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kIssue));
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kSrc>::kIssue));
+    set_registers<Regs<kSrc>::kIssue>();
     if (warp == kIssueWarp) {
       // ------------------------------------------------------------------ the products
       const uint32_t idesc_s = idesc_f16(1u, 0u, (uint32_t)kRows, (uint32_t)kTile);
@@ -805,10 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t vd = sw128_desc(smem_u32(v_own(gi)), 16, 1024);
           constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
-          // (unrolled the products go out a third faster; quantised rows are slower still, and want the registers)
-          constexpr int kUnroll = kQuant ? 4 : 64;
+          // (unrolled: a loop over the blocks issues half to a third as fast)
           if (elect_one()) {
-#pragma unroll kUnroll
+#pragma unroll
             for (int i = 0; i < 4 * (kXBlocks + kYBlocks); ++i) {
               const int c = i >> 2;
               const uint64_t bd = (c < kXBlocks ? xd + (uint64_t)c * kc : yd + (uint64_t)(c - kXBlocks) * kc) + (uint64_t)(i & 3) * 2;
@@ -826,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&vo_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll kUnroll
+#pragma unroll
             for (int i = 4 * (kXBlocks + kYBlocks); i < 4 * kChunks; ++i)
               umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), vd + (uint64_t)((i >> 2) - kXBlocks - kYBlocks) * kc + (uint64_t)(i & 3) * 2, idesc_s);
             mma_commit(s_full);

@@ -106,7 +106,7 @@ def make_latent(kind, reqs, rows=None):
 
 def attend(q, values, d_v, tau, limits, kind):
     """Softmax attention of query rows q [m, H, d] over value rows [n, d], row i over the first
-    limits[i] of them; out, lse and their tolerances."""
+    limits[i] of them (0 and -inf where that is none); out, lse and their tolerances."""
     q64 = q.double()
     n = values.shape[0]
     z = torch.einsum("thd,sd->ths", q64, values) * tau
@@ -114,20 +114,21 @@ def attend(q, values, d_v, tau, limits, kind):
     hidden = torch.arange(n, device=q.device)[None, None, :] >= limits[:, None, None]
     z = z.masked_fill(hidden, -math.inf)
     lse = torch.logsumexp(z, -1)
-    p = torch.exp(z - lse[..., None])
+    p = torch.where(hidden, 0.0, torch.exp(z - lse[..., None]))
     out = p @ values[:, :d_v]
     A = p @ values[:, :d_v].abs()
-    E = (zabs * 600 * 2.0 ** -23 + z.abs() * 2.0 ** -22).masked_fill(hidden, 0.0).amax(-1)
+    lse_size = torch.where(lse == -math.inf, 0.0, lse.abs())
+    E = (zabs * 600 * 2.0 ** -23 + z.masked_fill(hidden, 0.0).abs() * 2.0 ** -22).masked_fill(hidden, 0.0).amax(-1)
     w = 2 * E + 2.0 ** -20
     if kind == "f32":
-        return out, lse, (2 * w + 2 * n * 2.0 ** -23)[..., None] * A + 2.0 ** -24 * out.abs(), w + n * 2.0 ** -23 + 2.0 ** -22 * lse.abs()
+        return out, lse, (2 * w + 2 * n * 2.0 ** -23)[..., None] * A + 2.0 ** -24 * out.abs(), w + n * 2.0 ** -23 + 2.0 ** -22 * lse_size
     tol = (2 * 2.0 ** -8 + 2 * w + n / 16 * 2.0 ** -23)[..., None] * A + 2.0 ** -8 * out.abs()
-    return out, lse, tol, 2.0 ** -8 + w + 2.0 ** -22 * lse.abs()
+    return out, lse, tol, 2.0 ** -8 + w + 2.0 ** -22 * lse_size
 
 
 def close(got, want, tol, what=""):
-    err = (got.double() - want).abs()
-    bad = ~(err <= tol)
+    g = got.double()
+    bad = ~((g == want) | ((g - want).abs() <= tol))
     if bool(bad.any()):
         i = tuple(bad.nonzero()[0].tolist())
         raise AssertionError("%s: %d of %d off, first at %s: got %r, want %r, tolerance %.3g" %

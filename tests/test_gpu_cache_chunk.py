@@ -743,3 +743,174 @@ def test_two_streams_with_their_own_workspaces():
     no_error()
     for i in range(2):
         check_chunk(reqs[i], qs[i], caches[i][0], caches[i][1], TAU, outs[i][0], outs[i][1], "q")
+
+
+# ------------------------------------------------------------------------------------------ both ways of reading quantised chunks
+
+
+def chunk_with(reqs, q, cache, full):
+    """Chunk attention with the whole workspace (quantised rows of several row tiles are expanded once)
+    or with none where a call needs none (each row tile turns them into bf16 itself)."""
+    T, H = q.shape[:2]
+    out = torch.full((T, H, 512), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    size = dsa.dsa_chunk_mla_workspace_size(T, len(reqs.news), H, 512, reqs.max_context)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") if full else None   # NaN wherever it is read unwritten
+    dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, out, lse, ws)
+    return out, lse
+
+
+@pytest.mark.parametrize("full", [True, False])
+def test_chunk_quantised_bad_rows_many_tiles(full):
+    # row tiles enough for one unit per SM and more, so that nothing is split: bad scales, a page outside the
+    # pool, a request without tokens, NaN codes, and garbage in every row that no request has
+    reqs = Requests([100, 5, 0, 300], [150, 0, 90, 40], seed=61, pad=2)
+    cache, values = make_latent("q", reqs)
+    q = randn(reqs, reqs.tokens, 128, 576, dtype=torch.bfloat16)
+    used = torch.zeros(reqs.num_blocks * PAGE, dtype=torch.bool, device="cuda")
+    for r in range(4):
+        used[reqs.rows(r)] = True
+    cache.data.view(-1, 640)[~used] = 0x7F
+    cache.scale.view(-1, 4)[~used] = math.nan
+    skipped = {0: [7, 110, 249], 2: [0, 33], 3: []}
+    for r, ps in skipped.items():
+        for i, p in enumerate(ps):
+            cache.scale.view(-1, 4)[reqs.rows(r, p, p + 1), i % 4] = 0.3
+    skipped[3] = list(range(64, 128))
+    rows3 = reqs.rows(3)
+    reqs.table[3, 1] = 1 << 28
+    nan_at = 120                                    # of request 0: its tokens from position 120 on get NaN
+    cache.data.view(-1, 640)[reqs.rows(0, nan_at, nan_at + 1), 300] = 0xFF
+    out, lse = chunk_with(reqs, q, cache, full)
+    assert dsa.dsa_get_device_error() == dsa.DEVERR_SCALE | dsa.DEVERR_BLOCK_ID
+    assert bool((out[reqs.total:] == 7.0).all()) and bool((lse[reqs.total:] == 7.0).all())
+    start = 0
+    for r, n in enumerate(reqs.news):
+        if n:
+            keep = torch.ones(reqs.lens[r], dtype=torch.bool, device="cuda")
+            keep[skipped[r]] = False
+            s = slice(start, start + (n if r else nan_at - reqs.ctxs[0]))
+            lim = keep.cumsum(0)[reqs.ctxs[r]:reqs.ctxs[r] + s.stop - s.start]
+            o, l, to, tl = attend(q[s], values[(rows3 if r == 3 else reqs.rows(r))[keep]], 512, TAU, lim, "q")
+            close(out[s], o, to, "out of request %d" % r)
+            close(lse[s], l, tl, "lse of request %d" % r)
+        start += n
+    tail = slice(nan_at - reqs.ctxs[0], reqs.news[0])
+    assert bool(out[tail].isnan().all()) and bool(lse[tail].isnan().all())
+
+
+def test_chunk_expanded_equals_unexpanded():
+    reqs = Requests([0, 700, 64], [200, 33, 150], seed=62)
+    cache, values = make_latent("q", reqs)
+    q = randn(reqs, reqs.total, 128, 576, dtype=torch.bfloat16)
+    a, b = chunk_with(reqs, q, cache, True), chunk_with(reqs, q, cache, False)
+    no_error()
+    # the same rows, products and order of sums
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_chunk(reqs, q, cache, values, TAU, a[0], a[1], "q")
+
+
+@pytest.mark.parametrize("kind", ["q", "bf16"])
+def test_chunk_ragged_splits(kind):
+    # requests of very different lengths whose row tiles are split: units handed out as CTAs become free; used twice,
+    # with a workspace that the first call has left dirty
+    reqs = Requests([6000, 40, 2500, 0, 900], [3, 4, 1, 2, 2], seed=63)
+    cache, values = make_latent(kind, reqs)
+    q = randn(reqs, reqs.total, 128, 576, dtype=torch.bfloat16)
+    size = dsa.dsa_chunk_mla_workspace_size(reqs.total, 5, 128, 512, reqs.max_context)
+    assert size > 0
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(2):
+        out, lse = torch.empty(reqs.total, 128, 512, dtype=q.dtype, device="cuda"), torch.empty(reqs.total, 128, device="cuda")
+        dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, out, lse, ws)
+        got.append((out, lse))
+    no_error()
+    check_chunk(reqs, q, cache, values, TAU, got[0][0], got[0][1], kind)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_chunk_workspace_is_checked():
+    reqs = Requests([4000], [2], seed=64)
+    cache, _ = make_latent("bf16", reqs)
+    q = randn(reqs, 2, 128, 576, dtype=torch.bfloat16)
+    out = torch.empty(2, 128, 512, dtype=torch.bfloat16, device="cuda")
+    size = dsa.dsa_chunk_mla_workspace_size(2, 1, 128, 512, reqs.max_context)
+    ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+    for bad in (None, ws[:size - 1], ws[1:1 + size]):
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, out, workspace=bad)
+    dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, out, workspace=ws[:size])
+    no_error()
+
+
+def test_two_captured_graphs_with_their_own_workspaces():
+    # the same call captured twice, replayed on two streams at once
+    reqs = Requests([2500, 300, 0], [4, 7, 3], seed=65)
+    cache, values = make_latent("q", reqs)
+    qs = [randn(reqs, reqs.total, 128, 576, dtype=torch.bfloat16) for _ in range(2)]
+    size = dsa.dsa_chunk_mla_workspace_size(reqs.total, 3, 128, 512, reqs.max_context)
+    runs = []
+    for q in qs:
+        ws = torch.full((max(size, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty(reqs.total, 128, 512, dtype=q.dtype, device="cuda"), torch.empty(reqs.total, 128, device="cuda")
+        call = lambda: dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, out, lse, ws)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((g, side, q, out, lse, ws))
+    for g, side, *_ in runs:
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                g.replay()
+    torch.cuda.synchronize()
+    no_error()
+    for _, _, q, out, lse, _ in runs:
+        check_chunk(reqs, q, cache, values, TAU, out, lse, "q")
+
+
+@pytest.mark.parametrize("heads", [1, 16, 128])
+def test_sparse_quantised_equals_bf16_values(heads):
+    # a quantised cache and a bf16 one with the same values give the same up to the order of sums
+    reqs = Requests([1200], [3], seed=66)
+    cache, values = make_latent("q", reqs)
+    plain = dsa.PagedCache(values.bfloat16().view(-1, PAGE, 576))
+    assert torch.equal(plain.data.double().view(-1, 576), values)
+    q = randn(reqs, 3, heads, 576, dtype=torch.bfloat16)
+    idx = selection(reqs, 256, 10, 1.0)
+    for c in (cache, plain):
+        out, lse = run_sparse(reqs, q, c, idx)
+        check_sparse(reqs, q, values, idx, out, lse)
+    no_error()
+
+
+def test_tensors_of_another_device_are_refused():
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one device")
+    reqs = Requests([10], [2], seed=67, device="cuda:0")
+    cache, _ = make_latent("q", reqs)
+    with torch.cuda.device(1), pytest.raises(ValueError):
+        dsa.dsa_cache_read(cache, reqs.chunks(), torch.empty(2, 576, device="cuda:0"))
+
+
+def test_empty_chunks_do_nothing():
+    reqs = Requests([10, 20], [0, 0], seed=68)
+    cache, _ = make_latent("q", reqs)
+    q = torch.empty(0, 16, 576, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, torch.empty(0, 16, 512, dtype=torch.bfloat16, device="cuda"))
+    dsa.dsa_cache_read(cache, reqs.chunks(), torch.empty(0, 576, device="cuda"))
+    dsa.dsa_cache_append(None, torch.empty(0, 576, device="cuda"), None, cache, reqs.chunks())
+    # rows that belong to no request
+    out = torch.full((3, 576), 7.0, device="cuda")
+    dsa.dsa_cache_read(cache, reqs.chunks(), out)
+    q = torch.zeros(3, 16, 576, dtype=torch.bfloat16, device="cuda")
+    o = torch.full((3, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    size = dsa.dsa_chunk_mla_workspace_size(3, 2, 16, 512, reqs.max_context)
+    dsa.dsa_chunk_mla(q, cache, reqs.chunks(), TAU, o, workspace=torch.empty(max(size, 1), dtype=torch.uint8, device="cuda"))
+    no_error()
+    assert bool((out == 7.0).all()) and bool((o == 7.0).all())
