@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // counters a warp waits by).  A key without a row reads row 0.
       const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // eight lanes: four pieces of both rows of a pair
       uint4 code[4];
-      float sc_own = 1.0f, sc_peer = 1.0f;
-      uint32_t seen_own = 0u, bad_own = 0u, none_peer = 0u;  // lanes: key with a row; no row, or a scale that is no power of two; no row
+      float sc_own = 1.0f;
+      uint32_t seen_own = 0u, bad_own = 0u;  // lanes: key with a row; no row, or a scale that is no power of two
       auto row_at = [&](int g, int which, int k8) -> int { return row_ring[(g % kSlots * 2 + which) * kTile + warp * kKeysPerWarp + k8]; };
       auto load_codes = [&](int g, int which, uint32_t h) {
         const uint8_t* base = p.data + 256 * h + 16 * l16;
@@ -330,32 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) put(Flag<false>(), q);
         }
       };
-      // the other page's V of step j (CTA step g): on its way ...
-      auto fetch_peer = [&](int g) {
-        sc_peer = load_scales(g, 1);
-        fetch(g, 1, v);
-        none_peer = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);
-      };
-      // ... and its codes into place
-      auto put_peer = [&](int g, int j) -> bool {
-        if (g >= 1 && !warp_wait(vp_empty, (g - 1) & 1, p.err, abort_flag)) return false;
-        const int base = x.lo + (2 * j + 1 - (int)v) * kTile;
-        const bool partly = kSrc != kSelected && base + kTile - 1 > x.tok0 && x.hi - 1 > max(x.tok0, base - 1);
-        uint32_t nan_rows = 0u;
-        load_codes(g, 1, v);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&r_empty[g % kSlots]);
-        const uint32_t bad = none_peer | __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc_peer) && ((uint32_t)(lane & 3) >> 1) == v);
-        put_all(sc_peer, bad, v, partly, v_peer + (l16 >> 2) * K_CHUNK, nan_rows);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&vp_full[g & 1]);
-        return true;
-      };
       if (kQuant && nsteps > 0) {
         if (!(ok = warp_wait(&r_full[gi % kSlots], (gi / kSlots) & 1, p.err, abort_flag))) break;
         sc_own = load_scales(gi, 0);
-        fetch(gi, 0, v ^ 1u);
         fetch(gi, 0, v);
         check_own(gi);
       }
@@ -402,68 +379,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ui;
 
       if constexpr (kQuant) {
-        for (int j = 0; j < nsteps; ++j, ++gi) {
+        // Three groups of codes a step, by one piece of code (three copies of it do not fit the instruction cache beside the
+        // other roles' loops): the own page's other half into X1 and Y, its this half into V, and, a step behind,
+        // the other page's this half into its V.
+#pragma unroll 1
+        for (int j = 0; j <= nsteps && ok; ++j) {
           const int s = gi & 1, slot = gi % kSlots;
-          const bool more = j + 1 < nsteps;
-          const bool partly = kSrc != kSelected && x.lo + (2 * j + (int)v + 1) * kTile - 1 > x.tok0 && x.hi - 1 > x.tok0;
-          uint32_t nan_rows = 0u;
-          const uint32_t bad = bad_own;
-          // X1 and Y: the own page's values of the other half; X0: its RoPE part as it is, in the background
-          if (gi >= 1 && (!(ok = warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag)) || !(ok = warp_wait(y_empty, (gi - 1) & 1, p.err, abort_flag)))) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r8 = 4 * i + (lane >> 3);
-            const int r = warp * kKeysPerWarp + r8;
-            cp_async_16(smem_u32(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
-                        p.data + (int64_t)max(0, row_at(gi, 0, r8)) * kLatentBytes + kDv + 16 * (lane & 7),
-                        ((bad >> (4 * r8)) & 0xFu) ? 0u : 16u);
-          }
-          load_codes(gi, 0, v ^ 1u);
-          put_all(sc_own, bad, v ^ 1u, partly, (l16 >> 2) == 3 ? x_st + K_CHUNK : y_st + (l16 >> 2) * K_CHUNK, nan_rows);
-          if (j > 0) fetch_peer(gi - 1);
-          // V: its values of this half
-          if (!(ok = vo_free(gi))) break;
-          load_codes(gi, 0, v);
-          put_all(sc_own, bad, v, partly, v_own(gi) + (l16 >> 2) * K_CHUNK, nan_rows);
           float sc_next = 1.0f;
-          if (more) {
-            if (!(ok = warp_wait(&r_full[(gi + 1) % kSlots], ((gi + 1) / kSlots) & 1, p.err, abort_flag))) break;
-            sc_next = load_scales(gi + 1, 0);
-            fetch(gi + 1, 0, v ^ 1u);
-          }
-          const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
-          if (lane == 0) {
-            uint32_t valid = 0xFFu;
-            if (bad) {
-              bool flag = false;
-              for (int r8 = 0; r8 < kKeysPerWarp; ++r8)
-                if ((bad >> (4 * r8)) & 0xFu) {
-                  valid &= ~(1u << r8);
-                  flag |= (seen_own >> (4 * r8)) & 1u;
-                }
-              if (flag) raise_error(p.err, DSA_DEVERR_SCALE);
+          uint32_t nan_rows = 0u;
+#pragma unroll 1
+          for (int part3 = j < nsteps ? 0 : 2; part3 < (j > 0 ? 3 : 2); ++part3) {
+            const bool other = part3 == 2;
+            const int g = other ? gi - 1 : gi;                       // step of the rows
+            const uint32_t h = part3 == 0 ? v ^ 1u : v;              // their half
+            const int base = x.lo + (2 * (other ? j - 1 : j) + (other ? 1 - (int)v : (int)v)) * kTile;
+            const bool partly = kSrc != kSelected && base + kTile - 1 > x.tok0 && x.hi - 1 > max(x.tok0, base - 1);
+            float sc = sc_own;
+            uint32_t bad = bad_own;
+            if (other) {
+              sc = load_scales(g, 1);
+              bad = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);
             }
-            masks[slot * 8 + warp] = (uint8_t)valid;
-            poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
+            load_codes(g, other, h);
+            uint8_t* dst = v_peer;
+            if (part3 == 0) {
+              if (gi >= 1 && (!(ok = warp_wait(x_empty, (gi - 1) & 1, p.err, abort_flag)) || !(ok = warp_wait(y_empty, (gi - 1) & 1, p.err, abort_flag)))) break;
+              // X0: the RoPE part as it is, in the background
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r8 = 4 * i + (lane >> 3);
+                const int r = warp * kKeysPerWarp + r8;
+                cp_async_16(smem_u32(x_st + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
+                            p.data + (int64_t)max(0, row_at(gi, 0, r8)) * kLatentBytes + kDv + 16 * (lane & 7),
+                            ((bad >> (4 * r8)) & 0xFu) ? 0u : 16u);
+              }
+              dst = (l16 >> 2) == 3 ? x_st + K_CHUNK - 3 * K_CHUNK : y_st;
+            } else if (part3 == 1) {
+              if (!(ok = vo_free(gi))) break;
+              dst = v_own(gi);
+            } else {
+              if (g >= 1 && !(ok = warp_wait(vp_empty, (g - 1) & 1, p.err, abort_flag))) break;
+              bad |= __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc) && ((uint32_t)(lane & 3) >> 1) == v);
+            }
+            put_all(sc, bad, h, partly, dst + (l16 >> 2) * K_CHUNK, nan_rows);
+            if (part3 == 0) continue;
+            if (part3 == 1) {
+              if (j + 1 < nsteps) {
+                if (!(ok = warp_wait(&r_full[(gi + 1) % kSlots], ((gi + 1) / kSlots) & 1, p.err, abort_flag))) break;
+                sc_next = load_scales(gi + 1, 0);
+                fetch(gi + 1, 0, v ^ 1u);
+                fetch(gi + 1, 0, v);
+              }
+              fetch(gi, 1, v);
+              const uint32_t poison = __reduce_or_sync(0xFFFFFFFFu, nan_rows);
+              if (lane == 0) {
+                uint32_t valid = 0xFFu;
+                if (bad) {
+                  bool flag = false;
+                  for (int r8 = 0; r8 < kKeysPerWarp; ++r8)
+                    if ((bad >> (4 * r8)) & 0xFu) {
+                      valid &= ~(1u << r8);
+                      flag |= (seen_own >> (4 * r8)) & 1u;
+                    }
+                  if (flag) raise_error(p.err, DSA_DEVERR_SCALE);
+                }
+                masks[slot * 8 + warp] = (uint8_t)valid;
+                poisons[slot * 8 + warp] = (uint8_t)(poison & valid);
+              }
+              cp_async_wait_all();
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (part3 == 1) {
+                mbar_arrive(&xy_full[s]);
+                mbar_arrive(&vo_full[s]);
+              } else {
+                mbar_arrive(&vp_full[g & 1]);
+                mbar_arrive(&r_empty[g % kSlots]);
+              }
+            }
           }
-          cp_async_wait_all();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&xy_full[s]);
-            mbar_arrive(&vo_full[s]);
-          }
-          // V of the other page, a step behind
-          if (j > 0 && !(ok = put_peer(gi - 1, j - 1))) break;
-          if (more) {
-            fetch(gi + 1, 0, v);
+          if (!ok) break;
+          if (j + 1 < nsteps) {
             sc_own = sc_next;
             check_own(gi + 1);
           }
-        }
-        if (ok && nsteps > 0) {
-          fetch_peer(gi - 1);
-          ok = put_peer(gi - 1, nsteps - 1);
+          if (j < nsteps) ++gi;
         }
       } else {
       // --- copies.  A page: its first position, its number (-1: none), its rows that may be read.
