@@ -82,7 +82,8 @@ typedef void* dsa_stream; /* cudaStream_t */
  * bf16; `scale` is [num_blocks, 64, 4] f32, 16-byte aligned: element i < 512 of a row has the value
  * code[i] * scale[i / 128].  A scale is a power of two, 2^e with -100 <= e <= 119, so every value
  * is exact in bf16 and the attention kernels multiply by the very values the cache stands for.
- * A row takes 656 bytes instead of 1152. */
+ * A row takes 656 bytes instead of 1152.  The attention accumulates weights of up to 2^8 times values in
+ * f32: values beyond 2^109 may overflow there. */
 typedef struct dsa_paged_cache {
   const void* data;
   const float* scale;
@@ -243,8 +244,8 @@ size_t dsa_mla_workspace_size(int32_t num_queries, int32_t H, int32_t d_v, int32
  * request r has the rows cu_tokens[r] .. cu_tokens[r+1]-1 (device int32 [num_reqs + 1],
  * non-decreasing; a request may have none) and seq_len[r] tokens in its cache once the chunk is in
  * it (device int32 [num_reqs]), so its n rows sit at the positions seq_len[r]-n .. seq_len[r]-1.
- * Rows from cu_tokens[num_reqs] on belong to no request (a padded batch): inputs there are not
- * read, outputs are left as they are.  block_table: device int32 [num_reqs, max_blocks];
+ * Rows from cu_tokens[num_reqs] on belong to no request (a padded batch): inputs there have no
+ * effect, outputs are left as they are.  block_table: device int32 [num_reqs, max_blocks];
  * max_context: host bound, every seq_len[r] <= max_context <= max_blocks * 64.
  * A row whose request has cu_tokens or seq_len outside these bounds sets DSA_DEVERR_REQUEST and is
  * treated as a row behind the last one.  The arrays are read on the device: a captured call
@@ -272,7 +273,8 @@ typedef struct dsa_chunks {
  * the scale 2^e with the smallest e such that |x| <= 448 * 2^e for all of it, -100 <= e <= 119 (1
  * for a group of zeros), and the codes nearest to x / 2^e (ties to even, saturating).  An infinity
  * or NaN in a quantised group sets DSA_DEVERR_NONFINITE and is stored as NaN; it does not enter
- * the group's scale.  RoPE elements are stored as given.
+ * the group's scale.  RoPE elements are stored as given.  A token whose block id is outside the pool
+ * sets DSA_DEVERR_BLOCK_ID and is not written.
  * Every row is written by one warp; two tokens of one call in one slot (only block tables that
  * share a block that is being written can cause it) leave a mixture of the two rows there.
  */
@@ -302,9 +304,10 @@ dsa_status dsa_cache_read(const dsa_paged_cache* cache, const dsa_chunks* chunks
  * q: device [num_tokens, H, d_v + d_rope] of q_dtype; latent: dim == d_v + d_rope, dtype == q_dtype
  * (f32 or bf16) or DSA_LATENT_E4M3 (d_v 512, d_rope 64; q bf16 or f32); out: device [num_tokens,
  * H, d_v] of q_dtype; lse: device f32 [num_tokens, H] or NULL.
- * workspace: at least dsa_chunk_mla_workspace_size(...) bytes, 256-byte aligned (NULL when 0);
- * calls that may overlap on the GPU need one each.
- * A row of the cache that holds infinities or NaN reaches only the tokens that see it.  A block id
+ * workspace: dsa_chunk_mla_workspace_size(...) bytes, 256-byte aligned (NULL when 0); calls that may
+ * overlap on the GPU need one each.  Its contents need not be kept or cleared between calls.
+ * A row of the cache that holds infinities or NaN reaches only the tokens that see it (their results are
+ * NaN, or what the formula gives for an infinity).  A block id
  * outside the pool sets DSA_DEVERR_BLOCK_ID, a quantised row with a bad scale DSA_DEVERR_SCALE; the
  * row is skipped.  A token all of whose rows are skipped gets out = 0, lse = -inf.
  * Tensor cores: H <= 1024, d_v == 512, d_rope == 64, bf16 q and 16-byte aligned q and out.
@@ -314,7 +317,11 @@ dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v,
                          float softmax_scale, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, dsa_stream stream);
 
-/* Bytes of workspace dsa_chunk_mla needs for these sizes (0 when none).  Host only. */
+/* Bytes of workspace for dsa_chunk_mla with these sizes (0 when none).  Host only.  The partial results of
+ * split row tiles, and, with at least three 128-row tiles per request, room for the quantised rows of
+ * num_reqs * max_context positions in bf16 where that is at most 256 MiB: a call uses it for a quantised
+ * cache (its rows are then turned into bf16 once, not once per tile) and does without it when the
+ * workspace holds the partials only; a smaller workspace is an error. */
 size_t dsa_chunk_mla_workspace_size(int32_t num_tokens, int32_t num_reqs, int32_t H, int32_t d_v,
                                     int32_t max_context);
 

@@ -363,8 +363,8 @@ def dsa_cache_append(k, kv, keys: Optional[PagedCache], latent: Optional[PagedCa
         if kv.shape[0] != T or kv.dtype is not x.dtype:
             raise ValueError("k and kv must have the same tokens and dtype")
     cc = chunks._c(T)
-    dev = _same_device(k, kv, chunks.cu_tokens, keys.data if keys is not None else None,
-                       latent.data if latent is not None else None)
+    dev = _same_device(k, kv, chunks.cu_tokens, chunks.seq_len, chunks.block_table, keys and keys.data,
+                       keys and keys.scale, latent and latent.data, latent and latent.scale)
     if T == 0:
         return
     status = lib.dsa_cache_append(kp, ks, vp, vs, _dtype_code(x), kc, lc, cc, _raw_stream(dev) if stream is None else _stream(stream))
@@ -381,7 +381,7 @@ def dsa_cache_read(cache: PagedCache, chunks: Chunks, out, stream=None):
         raise ValueError("out must be [num_tokens, %d]" % c.dim)
     T = out.shape[0]
     cc = chunks._c(T)
-    dev = _same_device(cache.data, out, chunks.cu_tokens)
+    dev = _same_device(cache.data, cache.scale, out, chunks.cu_tokens, chunks.seq_len, chunks.block_table)
     if T:
         status = lib.dsa_cache_read(c, cc, _dev_ptr(out, "out"), _dtype_code(out),
                                     _raw_stream(dev) if stream is None else _stream(stream))
@@ -393,7 +393,7 @@ def dsa_cache_read(cache: PagedCache, chunks: Chunks, out, stream=None):
 def dsa_chunk_mla(q, latent: PagedCache, chunks: Chunks, softmax_scale, out, lse=None, workspace=None, stream=None):
     """Dense MQA-mode MLA of chunks of new tokens: the token at position p attends to the positions
     0..p of its request (include/dsa.h).  q [num_tokens, H, 576], out [num_tokens, H, 512],
-    workspace of dsa_chunk_mla_workspace_size(...) bytes."""
+    workspace of dsa_chunk_mla_workspace_size(...) bytes (uint8, its own for calls that may overlap)."""
     lib = load_library()
     T, H, dqk = q.shape
     d_v = out.shape[-1]
@@ -402,7 +402,7 @@ def dsa_chunk_mla(q, latent: PagedCache, chunks: Chunks, softmax_scale, out, lse
     if lse is not None and (lse.shape != (T, H) or lse.dtype is not torch.float32):
         raise ValueError("lse must be [num_tokens, H] float32")
     lc, cc = latent._c(), chunks._c(T)
-    dev = _same_device(q, latent.data, out, lse, workspace, chunks.cu_tokens)
+    dev = _same_device(q, latent.data, latent.scale, out, lse, workspace, chunks.cu_tokens, chunks.seq_len, chunks.block_table)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if T:
         status = lib.dsa_chunk_mla(_dev_ptr(q, "q"), _dtype_code(q), H, d_v, dqk - d_v, lc, cc, float(softmax_scale),

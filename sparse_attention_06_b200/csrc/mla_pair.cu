@@ -19,7 +19,7 @@
 // Per step and CTA: Q K^T of 64 keys (36 products of N = 64, ~1340 cycles), P V of 128 keys (8 of N = 256, 1024), into
 // shared memory the own page's nine 64-dim column blocks (72 KB) and this half's four of the other page (32 KB).
 // What bounds it: over bf16 rows the shared-memory port (~2800 of ~3500 cycles a step: the copies in, the products'
-// operands, P); over quantised rows the warps that turn codes into bf16 (~6500 cycles a step).
+// operands, P); over quantised rows the warps that turn codes into bf16 (~5500 cycles a step).
 //
 // Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
 // three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
@@ -47,8 +47,8 @@ using namespace packed;
 constexpr int kIssueWarp = kFillWarps + 4, kLookupWarp = kIssueWarp + 1;
 constexpr int kThreads = 32 * 16;
 // Registers a thread by warpgroup, 4 x 128 in all.  Spilled ones cost more than elsewhere: they miss the small L1
-// left beside 220 KB of shared memory (300 bytes of spill loads in the quantised fill: 1.06 -> 1.17 ms for a prefill of
-// 1024 queries).
+// left beside 220 KB of shared memory (300 bytes of spill loads in the quantised fill cost a prefill of 1024 queries a
+// tenth).
 template <Source kSrc>
 struct Regs {
   static constexpr bool kQuant = kSrc != kPagesBf16;
@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = (x.hi - x.lo + 2 * kTile - 1) / (2 * kTile);
 
       // --- Quantised rows.  A warp has eight keys of either page, pair q its keys 2 q + half; a lane has 16 codes of a
-      // row in one half of the values.  Lane l has the scale of key l / 4, group l % 4.  Codes are fetched into L1 one or
-      // two conversions ahead of their load (in registers they would be 48 more, and loads in flight share the few
-      // counters a warp waits by).  A key without a row reads row 0.
+      // row in one half of the values.  Lane l has the scale of key l / 4, group l % 4.  Codes are fetched into L2 some
+      // conversions ahead of their load (decode of 64 queries 86 -> 82 us; ahead in registers they spill, and come no
+      // sooner).  A key without a row reads row 0.
       const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // eight lanes: four pieces of both rows of a pair
       uint4 code[4];
       float sc_own = 1.0f;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto fetch = [&](int g, int which, uint32_t h) {
         const uint8_t* a = p.data + (int64_t)max(0, row_at(g, which, lane >> 2)) * kLatentBytes + 256 * h + 64 * (lane & 3);
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(a));  // (a row's 256 bytes: four lanes)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a));  // (a row's 256 bytes: four lanes)
       };
       auto load_scales = [&](int g, int which) -> float {
         return loadf_here(p.scale + (int64_t)max(0, row_at(g, which, lane >> 2)) * 4 + (lane & 3));
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       if constexpr (kQuant) {
         // Three groups of codes a step, by one piece of code (three copies of it do not fit the instruction cache beside the
-        // other roles' loops): the own page's other half into X1 and Y, its this half into V, and, a step behind,
+        // other roles' loops: prefill of 1024 queries 871 -> 1040 us): the own page's other half into X1 and Y, its this half into V, and, a step behind,
         // the other page's this half into its V.
 #pragma unroll 1
         for (int j = 0; j <= nsteps && ok; ++j) {
@@ -980,6 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   __syncthreads();
+  if (*abort_flag) {  // gave up: what is on its way to the other CTA gets a millisecond to arrive
+    for (const long long t0 = clock64(); clock64() - t0 < 2000000LL;) {
+    }
+  }
   cluster_sync_all();  // nothing of the other CTA is on its way here any more
   if (warp == kIssueWarp) {
     tc_fence_after();
