@@ -497,15 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto copy = [&](const Page& a, bool whole, int row, int lo, int hi, uint8_t* dst, uint64_t* bar) {
         if (whole) {
           if (warp == 0 && lane == 0)
+#pragma unroll 1
             for (int c = lo; c < hi; ++c) tma_load_2d(dst + (c - lo) * K_CHUNK, &pmap, bar, block_of(c, v) * 64, a.page * kTile);
           return;
         }
-#pragma unroll
+#pragma unroll 1
         for (int g4 = 0; g4 < 2; ++g4) {
           const int rc = row >= 0 ? row : p.oob_row;
           const int r0 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4), r1 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 1);
           const int r2 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 2), r3 = __shfl_sync(0xFFFFFFFFu, rc, 4 * g4 + 3);
           if (lane == 0)
+#pragma unroll 1
             for (int c = lo; c < hi; ++c)
               tma_gather4(dst + (c - lo) * K_CHUNK + (warp * kKeysPerWarp + 4 * g4) * 128, &rmap, bar, block_of(c, v) * 64, r0, r1, r2, r3);
         }
@@ -551,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (partly) {
           if (!warp_wait(&land_p[s], nland_p[s] & 1, p.err, abort_flag)) return false;
           ++nland_p[s];
+#pragma unroll 1
           for (int c = 0; c < kVBlocks; ++c) scan(peer, v_peer + c * K_CHUNK, true);
           fence_proxy_async_smem();
           __syncwarp();
@@ -592,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // values that are not finite become zero in the V blocks and their row is noted: the softmax makes
           // the weights of the tokens that see it NaN.  (In X and Y a NaN only reaches logits, of hidden keys masked ones.)
           uint32_t poison = 0u;
-          for (int c = 0; c < kVBlocks; ++c) poison |= scan(own, v_own(gi) + c * K_CHUNK, true);
-          poison |= scan(own, x_st + K_CHUNK, false);
-          for (int c = 0; c < kYBlocks; ++c) poison |= scan(own, y_st + c * K_CHUNK, false);
+#pragma unroll 1
+          for (int c = 1; c < kChunks; ++c)
+            poison |= scan(own, (c == 1 ? x_st : c < 5 ? y_st - 2 * K_CHUNK : v_own(gi) - 5 * K_CHUNK) + c * K_CHUNK, c >= 5);
           if (lane == 0) poisons[slot * 8 + warp] = (uint8_t)poison;
           fence_proxy_async_smem();
           __syncwarp();
@@ -679,10 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(s_empty);
         if (!__all_sync(0xFFFFFFFFu, valid == ~0ull && poison == 0ull)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            if ((poison >> c) & 1u) sv[c] = 0x7FC00000u;
+          for (int c = 0; c < 64; ++c)
             if (!((valid >> c) & 1u)) sv[c] = 0xFF800000u;
-          }
+          if (valid & poison) sv[0] = 0x7FC00000u;  // (one NaN weight makes the row's results NaN)
         }
         float mx[4];
 #pragma unroll
