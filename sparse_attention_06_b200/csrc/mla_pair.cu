@@ -135,6 +135,13 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, int
   }
   return __all_sync(0xFFFFFFFFu, ok);
 }
+__device__ __forceinline__ void umma_ss_acc(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc));
+}
 // arrive on `bar` of both CTAs once every product issued so far by this thread has completed
 __device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
   asm volatile(
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // --- Q of the unit: places 0 .. 2 of the block order to shared memory, the other six through X, the
       // first two thirds of Y and the own page's two V stages to tensor memory
-      uint8_t* stage_at[6] = {x_st, y_st, v_own(0), v_own(0) + Q_CHUNK, v_own(1), v_own(1) + Q_CHUNK};
+      auto stage_at = [&](int b) { return b == 0 ? x_st : b == 1 ? y_st : smem + OFF_V + (b - 2) * Q_CHUNK; };
       auto vo_free = [&](int g) { return g < 2 || warp_wait(&vo_empty[g & 1], ((g / 2) - 1) & 1, p.err, abort_flag); };
       if (ui >= 1 && !(ok = warp_wait(q_empty, (ui - 1) & 1, p.err, abort_flag))) break;
       if (!(ok = vo_free(gi)) || !(ok = vo_free(gi + 1))) break;
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(q_stage, kChunks * Q_CHUNK);
 #pragma unroll
-        for (int c = kSmemQ; c < kChunks; ++c) tma_load_2d(stage_at[c - kSmemQ], &qmap, q_stage, block_of(c, v) * 64, x.row0);
+        for (int c = kSmemQ; c < kChunks; ++c) tma_load_2d(stage_at(c - kSmemQ), &qmap, q_stage, block_of(c, v) * 64, x.row0);
         for (int c = 0; c < kSmemQ; ++c) tma_load_2d(q_s + c * Q_CHUNK, &qmap, q_stage, block_of(c, v) * 64, x.row0);
         staged = true;
       }
@@ -356,9 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       staged = false;
       {
         const int r = quarter * 32 + lane;
-#pragma unroll
+        // (written out it makes the quantised forms spill: sparse prefill of 1024 queries 825 -> 833 us; rolled up it costs
+        // the bf16 form more than it saves: 512 tokens at 16k context 1101 -> 1116 us)
+#pragma unroll(kQuant ? 1 : 6)
         for (int b = 0; b < 6; ++b) {  // this warp's half (64 bytes) of the row's block
-          const uint8_t* src = stage_at[b] + r * 128;
+          const uint8_t* src = stage_at(b) + r * 128;
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -831,19 +840,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t vd = sw128_desc(smem_u32(v_own(gi)), 16, 1024);
           constexpr uint64_t kc = K_CHUNK >> 4, qc = Q_CHUNK >> 4;
-          // (unrolled: a loop over the blocks issues half to a third as fast)
+          // place c of the block order, 16 dims (32 bytes, 8 tensor-memory columns) per product.  Loops over the blocks: the
+          // hot code of all roles has to fit the instruction cache (all 36 products written out: 1110 -> 1138 us for 512
+          // tokens at 16k context).
           if (elect_one()) {
+#pragma unroll 1
+            for (int c = 0; c < kSmemQ; ++c) {
+              const uint64_t bd = c < kXBlocks ? xd + (uint64_t)c * kc : yd, ad = qd + (uint64_t)c * qc;
+              umma_ss_acc(d_s, ad, bd, idesc_s, c > 0);
 #pragma unroll
-            for (int i = 0; i < 4 * (kXBlocks + kYBlocks); ++i) {
-              const int c = i >> 2;
-              const uint64_t bd = (c < kXBlocks ? xd + (uint64_t)c * kc : yd + (uint64_t)(c - kXBlocks) * kc) + (uint64_t)(i & 3) * 2;
-              if (i == 0)
-                umma_ss<0>(d_s, qd, bd, idesc_s);
-              else if (c < kSmemQ)
-                umma_ss<1>(d_s, qd + (uint64_t)c * qc + (uint64_t)(i & 3) * 2, bd, idesc_s);
-              else
-                umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), bd, idesc_s);
-              if (i == 4 * kXBlocks - 1) mma_commit(x_empty);
+              for (int i = 1; i < 4; ++i) umma_ss<1>(d_s, ad + 2 * i, bd + 2 * i, idesc_s);
+              if (c == kXBlocks - 1) mma_commit(x_empty);
+            }
+#pragma unroll 1
+            for (int c = kSmemQ; c < kXBlocks + kYBlocks; ++c) {
+              const uint64_t bd = yd + (uint64_t)(c - kXBlocks) * kc;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) umma_ts<1>(d_s, a_q + (uint32_t)(32 * (c - kSmemQ) + 8 * i), bd + 2 * i, idesc_s);
             }
             mma_commit(y_empty);
           }
@@ -851,9 +864,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&vo_full[gi & 1], (gi / 2) & 1, p.err, abort_flag))) break;
           tc_fence_after();
           if (elect_one()) {
+#pragma unroll 2
+            for (int c = kXBlocks + kYBlocks; c < kChunks; ++c) {
+              const uint64_t bd = vd + (uint64_t)(c - kXBlocks - kYBlocks) * kc;
 #pragma unroll
-            for (int i = 4 * (kXBlocks + kYBlocks); i < 4 * kChunks; ++i)
-              umma_ts<1>(d_s, a_q + (uint32_t)((i - 4 * kSmemQ) * 8), vd + (uint64_t)((i >> 2) - kXBlocks - kYBlocks) * kc + (uint64_t)(i & 3) * 2, idesc_s);
+              for (int i = 0; i < 4; ++i) umma_ts<1>(d_s, a_q + (uint32_t)(32 * (c - kSmemQ) + 8 * i), bd + 2 * i, idesc_s);
+            }
             mma_commit(s_full);
             if (j == nsteps - 1) mma_commit(q_empty);
           }
