@@ -56,6 +56,7 @@ struct Params {
   int32_t num_blocks, oob_row;
   int T, H, k, ks, nsplit, per, prows, tiles, num_reqs, max_blocks, max_context;
   int* next;              // units handed out beyond the first of each CTA (zero at launch), or null: round robin
+  int cold;               // quantised rows are probably not in L2
   float scale_log2;       // softmax scale * log2(e)
   int* err;
 };

@@ -11,15 +11,19 @@
 //
 // The pair.  O of 128 rows x 512 values in f32 fills tensor memory, so the values are split over two CTAs; if each
 // computed S = Q K^T for itself, 576 of 1088 multiplications would be done twice (measured: 1.48 ms for 512 tokens x
-// 64 heads at 16k context, against 1.15 ms).  Here the two are a cluster: of every 128 keys (a step) each computes S and
+// 64 heads at 16k context, against 1.15 ms for the first form of this kernel and 1.10 ms now).  Here the two are a cluster: of every 128 keys (a step) each computes S and
 // P for its own 64-key page, and copies P to the other through distributed shared memory (16 KB a step); both multiply
 // the whole P (128 rows x 128 keys) with their half of the values.  Softmax bases have to agree: the rows' maxima of the
 // two pages are exchanged first (one f32 a row).
 //
 // Per step and CTA: Q K^T of 64 keys (36 products of N = 64, ~1340 cycles), P V of 128 keys (8 of N = 256, 1024), into
 // shared memory the own page's nine 64-dim column blocks (72 KB) and this half's four of the other page (32 KB).
-// What bounds it: over bf16 rows the shared-memory port (~2800 of ~3500 cycles a step: the copies in, the products'
-// operands, P); over quantised rows the warps that turn codes into bf16 (~5500 cycles a step).
+// What bounds it: over bf16 rows (~4000 cycles a step) the shared-memory port, busy for ~2800 of them with the copies in,
+// the products' operands and P, and the exchange between the CTAs; over quantised rows (~6000) the warps that turn codes
+// into bf16.  And the instruction cache: the roles' loops together have to fit it, so most are kept rolled up.
+// Measured: 512 tokens x 64 heads at 16k context 1.10 ms (1080 TFLOP/s); a prompt of 2048 tokens x 128 heads 0.65 ms (900);
+// 64 queries x 128 heads over 2048 selected quantised rows each 74 us (490), 1024 queries x 64 heads 0.80 ms (365: 64
+// heads fill half a tile).
 //
 // Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
 // three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
@@ -276,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // --- Quantised rows.  A warp has eight keys of either page, pair q its keys 2 q + half; a lane has 16 codes of a
       // row in one half of the values.  Lane l has the scale of key l / 4, group l % 4.  Codes are fetched into L2 some
-      // conversions ahead of their load (decode of 64 queries 86 -> 82 us; ahead in registers they spill, and come no
-      // sooner).  A key without a row reads row 0.
+      // conversions ahead of their load, unless they are there (the launch decides; loaded a group ahead into the registers that
+      // the last group leaves, decode of 64 queries takes 79 us for 73).  A key without a row reads row 0.
       const int half = (lane >> 2) & 1, l16 = (lane & 3) | (lane >> 3) << 2;  // eight lanes: four pieces of both rows of a pair
       uint4 code[4];
       float sc_own = 1.0f;
@@ -289,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) code[q] = load16_here(base + (int64_t)max(0, row_at(g, which, 2 * q + half)) * kLatentBytes);
       };
       auto fetch = [&](int g, int which, uint32_t h) {
+        if (kSrc == kSelected && !p.cold) return;
         const uint8_t* a = p.data + (int64_t)max(0, row_at(g, which, lane >> 2)) * kLatentBytes + 256 * h + 64 * (lane & 3);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a));  // (a row's 256 bytes: four lanes)
       };
@@ -389,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       if constexpr (kQuant) {
         // Three groups of codes a step, by one piece of code (three copies of it do not fit the instruction cache beside the
-        // other roles' loops: prefill of 1024 queries 871 -> 1040 us): the own page's other half into X1 and Y, its this half into V, and, a step behind,
-        // the other page's this half into its V.
+        // other roles' loops: prefill of 1024 queries 871 -> 1040 us): the own page's other half into X1 and Y, its this
+        // half into V, and, a step behind, the other page's this half into its V.
 #pragma unroll 1
         for (int j = 0; j <= nsteps && ok; ++j) {
           const int s = gi & 1, slot = gi % kSlots;
