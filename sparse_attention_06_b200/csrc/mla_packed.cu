@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
 // Quantised rows of a batch of chunks as bf16 rows, once, for row tiles that would each turn them into bf16 again:
 // a step of 128 keys costs the attention ~6000 cycles over quantised rows, ~4000 over bf16 ones.  One warp per position
 // of a request that has tokens; rows[(request, position)], rows of pages outside the pool are left out (never read).
-// Bound by memory: 15.5k rows (28 MB) in 10.7 us, cold.
+// Bound by memory: 15.5k rows (28 MB) in 9.4 us, cold.
 constexpr int kExpandWarps = 4;
 __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const uint8_t* data, const float* scale, int num_blocks,
                                                                    const dsa_chunks c, int linear_pages, __nv_bfloat16* rows,
@@ -183,8 +183,8 @@ int64_t chunk_tiles(int num_tokens, int num_reqs, int H) { return first_tile(num
 // its key tiles and a fixed ~7 (queries in, output out); units are spread evenly over the SMs but for about half a unit
 // at the end; several splits cost the combine's launch and the partials' way to memory and back.  Only max_context and
 // the numbers of tokens and requests are known here; of several requests the mean length is taken as 0.6 of the
-// longest.  (Measured: 7 requests of 71 to 308 tokens, 162 us in whole row tiles, 200 us in halves; 16 requests of 4
-// tokens 186 and 193 us; one token at 2k context 61 us whole, 21 us in 16 splits.)
+// longest.  (Measured: 7 requests of 71 to 308 tokens, 142 us in whole row tiles, 184 us in halves; 16 requests of 4
+// tokens 182 and 181 us; one token at 2k context 19 us in 16 splits, 61 us whole in an earlier form.)
 int chunk_mla_split_tiles(int num_tokens, int num_reqs, int H, int max_context, int num_sms) {
   // tiles in use if the tokens are spread evenly over the requests
   const int64_t per_req = ((int64_t)num_tokens * H + (int64_t)num_reqs * kRows - 1) / ((int64_t)num_reqs * kRows);
