@@ -7,28 +7,17 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mla_pair_layout.h"
 
 namespace dsa {
 namespace packed {
 
-constexpr int kDqk = 576, kDv = 512, kHalf = 256;
-constexpr int kRows = 128;               // query rows per tile (MMA M)
-constexpr int kTile = 64;                // keys per tile = tokens per page
-constexpr int kChunks = 9;               // 64-dim column blocks of a row
-constexpr int kSmemQ = 3;                // Q blocks in shared memory (the first that Q K^T uses), the rest in tensor memory
-constexpr int kFillWarps = 8, kKeysPerWarp = kTile / kFillWarps;
 constexpr int kLatentBytes = 640;        // data bytes of a quantised row
 
-// A tile's blocks in the order Q K^T uses them: X0 (RoPE), X1, Y0, Y1, Y2 (the values of the other
-// half), V0 .. V3 (this half's values).
-constexpr int kXBlocks = 2, kYBlocks = 3, kVBlocks = 4;
 __device__ __forceinline__ int block_of(int pos, int v) {  // column block of a row at place `pos` of that order
   return pos == 0 ? 8 : pos < 5 ? 4 * (1 - v) + (pos == 1 ? 3 : pos - 2) : 4 * v + pos - 5;
 }
 
-constexpr int K_CHUNK = kTile * 128;
-constexpr int K_BYTES = kChunks * K_CHUNK;
-constexpr int Q_CHUNK = kRows * 128;
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320, TM_COLS = 512;
 
 // Where a unit's keys come from.
@@ -37,8 +26,6 @@ enum Source {
   kPages,      // quantised rows at consecutive positions
   kPagesBf16,  // bf16 rows at consecutive positions
 };
-
-constexpr int kUnitSlots = 2;
 
 struct Params {
   const uint8_t* data;    // pool rows
@@ -72,7 +59,7 @@ struct Unit {
   int prow;       // first partial row
   int v;
 };
-static_assert(sizeof(Unit) == 40, "unit ring");
+static_assert(sizeof(Unit) == kUnitBytes, "unit ring");
 
 template <bool B>
 struct Flag {
@@ -262,7 +249,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float2 s, uint32_t& lo, uint
 }
 
 // O_v / l of this warp's 32 rows, columns [c_lo, c_hi) (multiples of 32), from tensor memory to the
-// partials (f32) or the output (bf16) through a 2 KB staging area: lane i stages 64 bytes of its row, its
+// partials (f32) or the output (bf16) through a 2 KB staging area of its own: lane i stages 64 bytes of its row, its
 // 16-byte pieces permuted against bank conflicts, then the warp writes whole 64-byte pieces of eight rows at a time.
 __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t lane_base, int quarter, int c_lo, int c_hi,
                                         uint8_t* stage, float inv, bool have_o) {

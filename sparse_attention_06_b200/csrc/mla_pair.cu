@@ -65,29 +65,6 @@ __device__ __forceinline__ void set_registers() {  // of this warp's warpgroup; 
   if constexpr (kRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-constexpr int P_BYTES = kRows * kTile * 2;
-constexpr int V_BYTES = kVBlocks * K_CHUNK;
-constexpr int OFF_Q = 0;
-constexpr int OFF_P = OFF_Q + kSmemQ * Q_CHUNK;            // [2]: of the page of CTA 0, of CTA 1
-constexpr int OFF_Y = OFF_P + 2 * P_BYTES;
-constexpr int OFF_X = OFF_Y + kYBlocks * K_CHUNK;
-constexpr int OFF_V = OFF_X + kXBlocks * K_CHUNK;          // [2] own page, [1] the other
-constexpr int OFF_BAR = OFF_V + 3 * V_BYTES;
-constexpr int NBAR = 48;
-constexpr int kSlots = 4;
-constexpr int OFF_MASK = OFF_BAR + NBAR * 8;               // [slot] keys of the own page with a row to see, a byte per fill warp
-constexpr int OFF_POISON = OFF_MASK + kSlots * 8;          // [slot] rows with NaN or infinity, see below
-constexpr int OFF_STATS = OFF_POISON + kSlots * 8;         // 1 / l of each row (last unit)
-constexpr int OFF_MAX = OFF_STATS + kRows * 4;             // [2][128] values of the other CTA's rows
-constexpr int OFF_UNIT = OFF_MAX + 2 * kRows * 4;          // [2] units in hand
-constexpr int OFF_ROWS = OFF_UNIT + kUnitSlots * 40;       // [slot] bf16: own page, other page, masks of their rows that may be
-                                                           // read; quantised: [2][64] pool row of each key of either, -1: none
-constexpr int OFF_MAIL = OFF_ROWS + kSlots * 2 * kTile * 4;           // [4] units from CTA 0
-constexpr int OFF_MISC = OFF_MAIL + 16;
-constexpr int SMEM = OFF_MISC + 16;
-static_assert(SMEM <= 232448, "shared memory budget");
-static_assert(OFF_ROWS % 16 == 0 && OFF_MASK % 8 == 0, "alignment");
-
 // ---- cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -630,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last) {
         if (!(ok = warp_wait(ep_last, 0, p.err, abort_flag))) break;
         tc_fence_after();
-        store_o(p, x, my_lanes, quarter, 64 + 96 * part, 160 + 96 * part, smem + OFF_V + warp * 2048, stats[quarter * 32 + lane], nsteps > 0);
+        store_o(p, x, my_lanes, quarter, 64 + 96 * part, 160 + 96 * part, smem + OFF_V + warp * kStageBytes, stats[quarter * 32 + lane], nsteps > 0);
         tc_fence_before();
       }
     }
@@ -654,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t peer_x_bar = peer_address(&x_bar[quarter], v ^ 1u), peer_p_full = peer_address(p_full, v ^ 1u);
-    uint8_t* p_mine = smem + OFF_P + v * P_BYTES + quarter * 4096;  // P of this warp's rows
+    uint8_t* p_mine = smem + p_offset((int)v, quarter);  // P of this warp's rows
     uint8_t* p_row = p_mine + (lane >> 3) * 1024 + (lane & 7) * 16;
     const uint32_t peer_p = peer_address(p_mine, v ^ 1u);
     const uint32_t peer_slot = peer_address(smem + OFF_MAX + r * 4, v ^ 1u);
@@ -742,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // to the other CTA as one 4 KB copy (stores of 16 bytes got through at ~9 bytes a cycle)
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) copy_to_peer(peer_p, p_mine, 4096u, peer_p_full);
+        if (lane == 0) copy_to_peer(peer_p, p_mine, (uint32_t)kWarpPBytes, peer_p_full);
         if (rescale && j > 0) {
           tc_fence_after();
 #pragma unroll 1
@@ -760,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(p_full, 4096u);  // and the other CTA's P of these 32 rows
+        if (lane == 0) mbar_arrive_expect_tx(p_full, (uint32_t)kWarpPBytes);  // and the other CTA's P of these 32 rows
       }
       if (!ok) break;
       float other;
@@ -778,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ep_last);
       }
-      store_o(p, x, lane_base, quarter, 0, last ? 64 : kHalf, smem + OFF_P + v * P_BYTES + quarter * 2048, inv, nsteps > 0);
+      store_o(p, x, lane_base, quarter, 0, last ? 64 : kHalf, smem + stage_offset((int)v, quarter), inv, nsteps > 0);
       if (v == 0 && r < x.rows) {
         if (x.splits == 1) {
           if (p.lse) p.lse[(int64_t)x.row0 + r] = lse;

@@ -1,0 +1,79 @@
+"""Cache and chunk operators where one row, unit or call could reach into another: units that follow each other on a CTA
+pair, rows that are skipped, first calls."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_06_b200 as dsa
+from _cache_chunk import PAGE, Requests, check_chunk, make_latent, randn, run_chunk
+
+pytestmark = pytest.mark.gpu
+
+TAU = 1.0 / math.sqrt(192.0)
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    torch.cuda.init()
+    dsa.dsa_clear_device_error()
+    yield
+    dsa.dsa_clear_device_error()
+
+
+def no_error():
+    assert dsa.dsa_get_device_error() == 0
+
+
+def sparse(reqs, q, cache, idx, rows=slice(None), entry="prefill"):
+    """Sparse attention of the chosen queries, each alone on the pool."""
+    T, H = q[rows].shape[:2]
+    out, lse = torch.empty(T, H, 512, dtype=q.dtype, device="cuda"), torch.empty(T, H, device="cuda")
+    batch = dsa.Batch(torch.tensor(reqs.req, dtype=torch.int32, device="cuda")[rows].contiguous(),
+                      torch.tensor(reqs.pos, dtype=torch.int32, device="cuda")[rows].contiguous(), reqs.table, reqs.max_context)
+    size = dsa.dsa_mla_workspace_size(T, H, 512, idx.shape[1])
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+    fn = dsa.dsa_sparse_mla_prefill if entry == "prefill" else dsa.dsa_sparse_mla_decode
+    fn(q[rows].contiguous(), cache, batch, idx[rows].contiguous(), TAU, out, lse, ws)
+    return out, lse
+
+
+def chosen(reqs, k, seed):
+    g = torch.Generator().manual_seed(seed)
+    idx = torch.full((reqs.total, k), -1, dtype=torch.int32)
+    for t, p in enumerate(reqs.pos):
+        n = min(k, p + 1)
+        idx[t, :n] = torch.randperm(p + 1, generator=g)[:n].sort().values
+    return idx.cuda()
+
+
+# ------------------------------------------------------------------------------------------ units behind each other
+
+
+@pytest.mark.parametrize("heads", [128, 64, 20])
+@pytest.mark.parametrize("k", [128, 640])
+def test_units_behind_each_other_equal_units_alone(heads, k):
+    # ten units a CTA pair, short ones among them, bit for bit what one unit a pair gives: no unit's outputs reach
+    # into the next one's weights, nor the other way round
+    reqs = Requests([700, 0], [700, 40], seed=71 + heads)
+    cache, _ = make_latent("q", reqs)
+    q = randn(reqs, reqs.total, heads, 576, dtype=torch.bfloat16)
+    idx = chosen(reqs, k, 1)
+    out, lse = sparse(reqs, q, cache, idx)
+    for at in range(0, reqs.total, 60):
+        rows = slice(at, min(at + 60, reqs.total))
+        o, l = sparse(reqs, q, cache, idx, rows)
+        assert torch.equal(out[rows], o) and torch.equal(lse[rows], l), at
+    no_error()
+
+
+@pytest.mark.parametrize("kind", ["q", "bf16"])
+def test_prompt_of_many_units_repeats_itself(kind):
+    # some seven units a pair, twice each: equal bits, and the definition's values
+    reqs = Requests([0, 129, 64], [300, 150, 77], seed=75)
+    cache, values = make_latent(kind, reqs)
+    q = randn(reqs, reqs.total, 128, 576, dtype=torch.bfloat16)
+    a, b = run_chunk(reqs, q, cache, TAU), run_chunk(reqs, q, cache, TAU)
+    no_error()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_chunk(reqs, q, cache, values, TAU, a[0], a[1], kind)
