@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t bad = bad_own;
             if (other) {
               sc = load_scales(g, 1);
-              bad = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);
+              bad = __ballot_sync(0xFFFFFFFFu, row_at(g, 1, lane >> 2) < 0);  // no row; below: or a bad scale
             }
             load_codes(g, other, h);
             uint8_t* dst = v_peer;
@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst = v_own(gi);
             } else {
               if (g >= 1 && !(ok = warp_wait(vp_empty, (g - 1) & 1, p.err, abort_flag))) break;
-              bad |= __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc) && ((uint32_t)(lane & 3) >> 1) == v);
+              // (of either half: the whole row is skipped, and a NaN code left of it would reach O as 0 * NaN)
+              bad |= __ballot_sync(0xFFFFFFFFu, !latent_scale_ok(sc));
             }
             put_all(sc, bad, h, partly, dst + (l16 >> 2) * K_CHUNK, nan_rows);
             if (part3 == 0) continue;

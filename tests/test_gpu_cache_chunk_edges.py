@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sparse_attention_06_b200 as dsa
-from _cache_chunk import PAGE, Requests, check_chunk, make_latent, randn, run_chunk
+from _cache_chunk import Requests, attend, check_chunk, close, make_latent, randn, run_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,55 @@ def test_prompt_of_many_units_repeats_itself(kind):
     no_error()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     check_chunk(reqs, q, cache, values, TAU, a[0], a[1], kind)
+
+
+# ------------------------------------------------------------------------------------------ rows that are skipped
+
+
+def spoil(cache, row, group):
+    """A bad scale for one group of a quantised row, and NaN codes under the good scales of the others."""
+    cache.scale.view(-1, 4)[row, group] = 0.3
+    codes = cache.data.view(-1, 640)[row, :512].view(4, 128)
+    codes[[g for g in range(4) if g != group], 5] = 0x7F
+    cache.data.view(-1, 640)[row, :512] = codes.flatten()
+
+
+@pytest.mark.parametrize("group", [0, 1, 2, 3])
+@pytest.mark.parametrize("heads", [32, 128])
+def test_chunk_skips_the_whole_of_a_bad_row(group, heads):
+    # rows of pages of either CTA of a pair, seen by every token and by some, expanded first (128 heads) and not
+    reqs = Requests([400], [6], seed=81)
+    cache, values = make_latent("q", reqs)
+    q = randn(reqs, 6, heads, 576, dtype=torch.bfloat16)
+    rows = reqs.rows(0)
+    skipped = [10, 70, 200, 300, 403]
+    for p in skipped:
+        spoil(cache, int(rows[p]), group)
+    out, lse = run_chunk(reqs, q, cache, TAU)
+    assert dsa.dsa_get_device_error() == dsa.DEVERR_SCALE
+    keep = torch.ones(406, dtype=torch.bool, device="cuda")
+    keep[skipped] = False
+    o, l, to, tl = attend(q, values[rows[keep]], 512, TAU, keep.cumsum(0)[400:], "q")
+    close(out, o, to, "out")
+    close(lse, l, tl, "lse")
+
+
+@pytest.mark.parametrize("group", [0, 1, 2, 3])
+@pytest.mark.parametrize("heads", [8, 64, 128])
+@pytest.mark.parametrize("entry", ["prefill", "decode"])
+def test_sparse_skips_the_whole_of_a_bad_row(group, heads, entry):
+    # the spoiled rows come in the first, second and last 64 selected rows
+    reqs = Requests([500], [2], seed=82)
+    cache, values = make_latent("q", reqs)
+    q = randn(reqs, 2, heads, 576, dtype=torch.bfloat16)
+    idx = chosen(reqs, 200, 3)
+    bad = idx[0, [3, 90, 199]].tolist()
+    for p in bad:
+        spoil(cache, int(reqs.rows(0)[p]), group)
+    out, lse = sparse(reqs, q, cache, idx, entry=entry)
+    assert dsa.dsa_get_device_error() == dsa.DEVERR_SCALE
+    for t in range(2):
+        at = torch.tensor([p for p in idx[t].tolist() if p not in bad], device="cuda")
+        o, l, to, tl = attend(q[t:t + 1], values[reqs.rows(0)[at]], 512, TAU, torch.tensor([at.numel()], device="cuda"), "q")
+        close(out[t:t + 1], o, to, "out")
+        close(lse[t:t + 1], l, tl, "lse")
