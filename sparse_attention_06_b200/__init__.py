@@ -165,7 +165,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 @dataclasses.dataclass
 class PagedCache:
     """A paged per-token cache: data [num_blocks, block_size, dim] (f32 / bf16 / e4m3 codes as
-    uint8), scale [num_blocks, block_size] f32 for e4m3.  A quantised latent cache has data
+    uint8), scale [num_blocks, block_size] (or [num_blocks, block_size, 1]) f32 for e4m3.  A quantised latent cache has data
     [num_blocks, 64, 640] uint8 (512 e4m3 codes, 64 RoPE elements in bf16) and scale
     [num_blocks, 64, 4] f32, powers of two (include/dsa.h)."""
     data: torch.Tensor
@@ -177,14 +177,16 @@ class PagedCache:
         return LATENT_E4M3_DIM if self._quantised_latent() else self.data.shape[2]
 
     def _quantised_latent(self) -> bool:
-        return self.scale is not None and self.scale.dim() == 3
+        # (scales [num_blocks, 64, 1] are a key cache's, one per row)
+        scale = self.scale
+        return scale is not None and scale.dim() == 3 and scale.shape[2] != 1 and _DTYPE_CODES.get(self.data.dtype) == DSA_E4M3
 
     def _c(self) -> _PagedCache:
         data, scale = self.data, self.scale
         nb, bs, dim = data.shape
         dtype = _dtype_code(data)
-        if scale is not None and scale.dim() == 3:
-            if dtype != DSA_E4M3 or dim != LATENT_E4M3_BYTES:
+        if self._quantised_latent():
+            if dim != LATENT_E4M3_BYTES:
                 raise ValueError("a quantised latent cache has data [num_blocks, 64, 640] uint8")
             if scale.dtype != torch.float32 or scale.shape != (nb, bs, 4):
                 raise ValueError("a quantised latent cache has scale [num_blocks, 64, 4] float32")

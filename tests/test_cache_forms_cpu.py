@@ -37,3 +37,31 @@ def test_key_scales_of_a_row_each_are_taken(scale):
 def test_unquantised_caches_do_not_look_at_a_scale(dtype):
     with pytest.raises(ValueError, match=TAKEN):
         dsa.PagedCache(keys(dtype=dtype), torch.zeros(1))._c()
+
+
+def test_key_scales_with_a_last_dimension_of_one_are_a_key_caches():
+    for dim in (128, 576, 640):
+        c = dsa.PagedCache(keys(dim=dim), torch.zeros(3, 64, 1))
+        assert c.dim == dim
+        with pytest.raises(ValueError, match=TAKEN):
+            c._c()
+    with pytest.raises(ValueError, match="float32"):
+        dsa.PagedCache(keys(), torch.zeros(3, 64, 1, dtype=torch.bfloat16))._c()
+
+
+def test_scales_of_groups_are_a_quantised_latent_caches():
+    c = dsa.PagedCache(keys(dim=640), torch.zeros(3, 64, 4))
+    assert c.dim == 576
+    with pytest.raises(ValueError, match=TAKEN):
+        c._c()
+    for data, scale in ((keys(), torch.zeros(3, 64, 4)), (keys(dim=640), torch.zeros(3, 64, 5)), (keys(dim=640), torch.zeros(2, 64, 4))):
+        with pytest.raises(ValueError, match="quantised latent"):
+            dsa.PagedCache(data, scale)._c()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_unquantised_caches_do_not_look_at_group_scales(dtype):
+    c = dsa.PagedCache(keys(dtype=dtype), torch.zeros(3, 64, 4))
+    assert c.dim == 128
+    with pytest.raises(ValueError, match=TAKEN):
+        c._c()

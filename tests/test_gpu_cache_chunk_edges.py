@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sparse_attention_06_b200 as dsa
-from _cache_chunk import Requests, attend, check_chunk, close, make_latent, randn, run_chunk
+from _cache_chunk import Requests, attend, check_chunk, close, make_latent, quantise, randn, run_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,31 @@ def test_sparse_skips_the_whole_of_a_bad_row(group, heads, entry):
         o, l, to, tl = attend(q[t:t + 1], values[reqs.rows(0)[at]], 512, TAU, torch.tensor([at.numel()], device="cuda"), "q")
         close(out[t:t + 1], o, to, "out")
         close(lse[t:t + 1], l, tl, "lse")
+
+
+# ------------------------------------------------------------------------------------------ forms of a cache
+
+
+@pytest.mark.parametrize("tail", [(), (1,)])
+def test_key_scales_in_either_shape(tail):
+    # [num_blocks, 64] and [num_blocks, 64, 1] are the same array
+    reqs = Requests([0, 60], [70, 9], seed=84)
+    k = randn(reqs, reqs.total, 128)
+    data = torch.zeros(reqs.num_blocks, 64, 128, dtype=torch.uint8, device="cuda")
+    scale = torch.ones(reqs.num_blocks, 64, *tail, device="cuda")
+    keys = dsa.PagedCache(data, scale)
+    dsa.dsa_cache_append(k, None, keys, None, reqs.chunks())
+    back = torch.empty(reqs.total, 128, device="cuda")
+    dsa.dsa_cache_read(keys, reqs.chunks(), back)
+    no_error()
+    v, s = quantise(k, 128)
+    assert torch.equal(back.double(), v * s)
+    q, w = randn(reqs, 1, 64, 128, dtype=torch.bfloat16), torch.ones(1, 64, device="cuda")
+    pos = torch.tensor([69], dtype=torch.int32, device="cuda")
+    scores = torch.zeros(1, 72, device="cuda")
+    dsa.dsa_indexer_scores(q, w, keys, dsa.Batch(torch.zeros_like(pos), pos, reqs.table, 70), scores)
+    no_error()
+    want = torch.relu(q[0].double() @ (v * s)[:70].T).sum(0)
+    # 128 exact products and 64 heads summed in f32; two e4m3 terms carry bf16 queries to 2^-8 relative
+    size = (q[0].double().abs() @ (v * s)[:70].T.abs()).sum(0)
+    close(scores[0, :70], want, 2.0 ** -8 * size, "scores")
