@@ -130,8 +130,9 @@ __device__ void mla_generic_row(const MlaArgs& a, const int32_t* block_table, in
       part = fmaf(qs[i], load_cached(a.latent, row, i), part);
     const float logit = block_sum(part, red) * a.scale;
     const float m_new = fmaxf(m, logit);
-    const float corr = expf(m - m_new);
-    const float pe = expf(logit - m_new);
+    // (-inf - -inf is NaN: before the first finite logit there is nothing to rescale, and -inf has no weight)
+    const float corr = m == m_new ? 1.0f : expf(m - m_new);
+    const float pe = logit == -INFINITY ? 0.0f : expf(logit - m_new);
     l = l * corr + pe;
 #pragma unroll
     for (int c = 0; c < kMaxVPerThread; ++c) {

@@ -157,3 +157,31 @@ def test_key_scales_in_either_shape(tail):
     # 128 exact products and 64 heads summed in f32; two e4m3 terms carry bf16 queries to 2^-8 relative
     size = (q[0].double().abs() @ (v * s)[:70].T.abs()).sum(0)
     close(scores[0, :70], want, 2.0 ** -8 * size, "scores")
+
+
+# ------------------------------------------------------------------------------------------ infinite logits
+
+
+@pytest.mark.parametrize("kind,q_dtype", [("f32", torch.float32), ("q", torch.float32), ("bf16", torch.bfloat16), ("q", torch.bfloat16)])
+@pytest.mark.parametrize("at", [0, 2])
+def test_a_logit_of_minus_infinity_has_no_weight(kind, q_dtype, at):
+    # exp(-inf) = 0 wherever the row comes, the first of all among them; a token that sees nothing else has the sum 0
+    reqs = Requests([0], [70], seed=85)
+    cache, values = make_latent(kind, reqs)
+    q = randn(reqs, 70, 6, 576, dtype=q_dtype)
+    q[:, :, 530] = 1.0
+    rows = reqs.rows(0)
+    if kind == "q":
+        cache.data.view(-1, 640)[rows[at]].view(torch.bfloat16)[256 + 530 - 512] = -math.inf
+    else:
+        cache.data.view(-1, 576)[rows[at], 530] = -math.inf
+    out, lse = run_chunk(reqs, q, cache, TAU)
+    no_error()
+    keep = torch.ones(70, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    first = 1 if at == 0 else 0
+    o, l, to, tl = attend(q[first:], values[rows[keep]], 512, TAU, keep.cumsum(0)[first:], "f32" if q_dtype is torch.float32 else kind)
+    close(out[first:], o, to, "out")
+    close(lse[first:], l, tl, "lse")
+    if at == 0:
+        assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all())
