@@ -185,3 +185,63 @@ def test_a_logit_of_minus_infinity_has_no_weight(kind, q_dtype, at):
     close(lse[first:], l, tl, "lse")
     if at == 0:
         assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+
+
+# ------------------------------------------------------------------------------------------ the normaliser
+
+
+def fine_tolerances(q, values, limits, tau, out, lse):
+    """Bounds for bf16 queries with the normaliser summed from the weights before their rounding to bf16.
+    lse: no rounded weights in it, so what moves it is the logits' error, 2 E + 2^-20 as in _cache_chunk.py, the sum
+    of n weights in f32 (n partial sums at most, each to 2^-24 of the whole: n * 2^-24) and the final logarithm and its
+    sum, 2^-22 * (|lse| + 1).
+    out: weights rounded to bf16 once (2^-8 * A, A = sum p |v|), logits (numerator and normaliser: 2 * (2 E + 2^-20) * A),
+    accumulation n / 16 * 2^-23 * A and n * 2^-24 * A, and the output's rounding 2^-8 * |out|."""
+    n = values.shape[0]
+    hidden = torch.arange(n, device=q.device)[None, None, :] >= limits[:, None, None]
+    z = torch.einsum("thd,sd->ths", q.double(), values) * tau
+    zabs = torch.einsum("thd,sd->ths", q.double().abs(), values.abs()) * tau
+    E = (zabs * 600 * 2.0 ** -23 + z.abs() * 2.0 ** -22).masked_fill(hidden, 0.0).amax(-1)
+    w = 2 * E + 2.0 ** -20
+    p = torch.where(hidden, 0.0, torch.exp(z - lse[..., None]))
+    A = p @ values[:, :512].abs()
+    return ((2.0 ** -8 + 2 * w + n / 16 * 2.0 ** -23 + n * 2.0 ** -24)[..., None] * A + 2.0 ** -8 * out.abs(),
+            w + n * 2.0 ** -24 + 2.0 ** -22 * (lse.abs() + 1))
+
+
+@pytest.mark.parametrize("kind", ["q", "bf16"])
+@pytest.mark.parametrize("ctx,new,heads", [(0, 90, 16), (2047, 1, 128), (3000, 5, 64), (700, 200, 24), (9000, 2, 128)])
+def test_chunk_normaliser_sums_unrounded_weights(kind, ctx, new, heads):
+    reqs = Requests([ctx, 130], [new, 3], seed=86 + ctx)
+    cache, values = make_latent(kind, reqs)
+    # logits of a few tenths: every key counts, so that a lost or rounded weight shows
+    q = (randn(reqs, reqs.total, heads, 576) * 0.2).bfloat16()
+    out, lse = run_chunk(reqs, q, cache, TAU)
+    no_error()
+    start = 0
+    for r, n in enumerate(reqs.news):
+        v, s = values[reqs.rows(r)], slice(start, start + n)
+        limits = reqs.ctxs[r] + 1 + torch.arange(n, device="cuda")
+        o, l, _, _ = attend(q[s], v, 512, TAU, limits, kind)
+        to, tl = fine_tolerances(q[s], v, limits, TAU, o, l)
+        close(out[s], o, to, "out of request %d" % r)
+        close(lse[s], l, tl, "lse of request %d" % r)
+        start += n
+
+
+@pytest.mark.parametrize("heads", [128, 64, 12])
+@pytest.mark.parametrize("entry", ["prefill", "decode"])
+def test_sparse_normaliser_sums_unrounded_weights(heads, entry):
+    reqs = Requests([3000], [3], seed=87)
+    cache, values = make_latent("q", reqs)
+    q = (randn(reqs, 3, heads, 576) * 0.2).bfloat16()
+    idx = chosen(reqs, 2048, 4)
+    out, lse = sparse(reqs, q, cache, idx, entry=entry)
+    no_error()
+    for t in range(3):
+        v = values[reqs.rows(0)[idx[t].long()]]
+        limits = torch.tensor([2048], device="cuda")
+        o, l, _, _ = attend(q[t:t + 1], v, 512, TAU, limits, "q")
+        to, tl = fine_tolerances(q[t:t + 1], v, limits, TAU, o, l)
+        close(out[t:t + 1], o, to, "out")
+        close(lse[t:t + 1], l, tl, "lse")
