@@ -245,3 +245,69 @@ def test_sparse_normaliser_sums_unrounded_weights(heads, entry):
         to, tl = fine_tolerances(q[t:t + 1], v, limits, TAU, o, l)
         close(out[t:t + 1], o, to, "out")
         close(lse[t:t + 1], l, tl, "lse")
+
+
+# ------------------------------------------------------------------------------------------ calls behind each other
+
+
+@pytest.mark.parametrize("heads", [128, 16])
+def test_calls_behind_each_other_see_what_the_last_one_wrote(heads):
+    # one graph of 48 decode steps with nothing between the calls: the token's row is written, attended to densely and by
+    # selection, and read back, next to rows (and scales, in the same sectors) that the step before has read
+    steps, ctx = 48, 150
+    reqs = Requests([ctx + steps - 1], [1], seed=88)
+    cache, _ = make_latent("q", reqs)
+    fresh = (cache.data.clone(), cache.scale.clone())
+    kv = randn(reqs, steps, 576, dtype=torch.bfloat16)
+    q = randn(reqs, steps, heads, 576, dtype=torch.bfloat16)
+    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    lens = [torch.tensor([ctx + i + 1], dtype=torch.int32, device="cuda") for i in range(steps)]
+    chunks = [dsa.Chunks(one, n, reqs.table, reqs.max_context) for n in lens]
+    batches = [dsa.Batch(one[:1], n - 1, reqs.table, reqs.max_context) for n in lens]
+    idx = torch.full((steps, 256), -1, dtype=torch.int32)
+    for i in range(steps):
+        idx[i, :100] = torch.arange(ctx + i + 1 - 100, ctx + i + 1)
+    idx = idx.cuda()
+    dense, some = (torch.zeros(steps, heads, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse, lse2 = (torch.zeros(steps, heads, device="cuda") for _ in range(2))
+    back = torch.zeros(steps, 576, dtype=torch.bfloat16, device="cuda")
+    size = max(dsa.dsa_chunk_mla_workspace_size(1, 1, heads, 512, reqs.max_context), dsa.dsa_mla_workspace_size(1, heads, 512, 256), 1)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def step(i):
+        s = slice(i, i + 1)
+        dsa.dsa_cache_append(None, kv[s], None, cache, chunks[i])
+        dsa.dsa_chunk_mla(q[s], cache, chunks[i], TAU, dense[s], lse[s], ws)
+        dsa.dsa_sparse_mla_decode(q[s], cache, batches[i], idx[s], TAU, some[s], lse2[s], ws)
+        dsa.dsa_cache_read(cache, chunks[i], back[s])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(0)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(steps):
+            step(i)
+    v, s = quantise(kv[:, :512], 128)
+    new = torch.cat([v * s.repeat_interleave(128, 1), kv[:, 512:].double()], 1)
+    for _ in range(5):
+        # the rows to come hold other values until their step writes them
+        cache.data.copy_(fresh[0])
+        cache.scale.copy_(fresh[1])
+        before = torch.empty(ctx, 576, dtype=torch.float32, device="cuda")
+        dsa.dsa_cache_read(cache, dsa.Chunks(torch.tensor([0, ctx], dtype=torch.int32, device="cuda"),
+                                             torch.tensor([ctx], dtype=torch.int32, device="cuda"), reqs.table, reqs.max_context), before)
+        values = torch.cat([before.double(), new])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(back.double(), new)
+        o, l, to, tl = attend(q, values, 512, TAU, ctx + 1 + torch.arange(steps, device="cuda"), "q")
+        close(dense, o, to, "dense")
+        close(lse, l, tl, "lse, dense")
+        for i in range(steps):
+            o, l, to, tl = attend(q[i:i + 1], values[ctx + i + 1 - 100:ctx + i + 1], 512, TAU, torch.tensor([100], device="cuda"), "q")
+            close(some[i:i + 1], o, to, "selected")
+            close(lse2[i:i + 1], l, tl, "lse, selected")
+    no_error()
