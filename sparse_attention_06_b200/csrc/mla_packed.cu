@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
   for (int sp0 = 0; sp0 < n; sp0 += 16) {
     float4 a[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) a[e] = sp0 + e < n ? __ldg(src + (sp0 + e) * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < 16; ++e) a[e] = sp0 + e < n ? src[(sp0 + e) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float w = sp0 + e < n ? wts[sp0 + e] : 0.0f;
@@ -109,11 +109,11 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const uint8_t
   float s[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    w[h] = __ldg(reinterpret_cast<const uint2*>(src + 256 * h) + lane);
-    s[h] = __ldg(scale + row * 4 + 2 * h + (lane >> 4));
+    w[h] = reinterpret_cast<const uint2*>(src + 256 * h)[lane];
+    s[h] = scale[row * 4 + 2 * h + (lane >> 4)];
   }
   uint4 rope;
-  if (lane < 8) rope = __ldg(reinterpret_cast<const uint4*>(src + kDv) + lane);
+  if (lane < 8) rope = reinterpret_cast<const uint4*>(src + kDv)[lane];
   const bool ok = __all_sync(0xFFFFFFFFu, latent_scale_ok(s[0]) && latent_scale_ok(s[1]));
   if (lane == 0) {
     row_ok[i] = ok;

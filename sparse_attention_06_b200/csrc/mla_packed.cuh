@@ -83,15 +83,15 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
 }
 
 // Loads that stay where they are written: left to itself the compiler moves loads for later down to their use, and
-// with them their whole latency.
+// with them their whole latency.  (Not the non-coherent path: the kernel that writes the rows may end after this one began.)
 __device__ __forceinline__ uint4 load16_here(const void* a) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
   return v;
 }
 __device__ __forceinline__ float loadf_here(const float* a) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(a));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(a));
   return v;
 }
 
