@@ -42,7 +42,7 @@ struct Params {
   int linear_pages;       // ... whose pages follow each other, so many for each request; 0: pages of the pool
   int32_t num_blocks, oob_row;
   int T, H, k, ks, nsplit, per, prows, tiles, num_reqs, max_blocks, max_context;
-  int* next;              // units handed out beyond the first of each CTA (zero at launch), or null: round robin
+  int* next;              // units handed out beyond the first of each CTA pair (zero at launch), or null: round robin
   int cold;               // quantised rows are probably not in L2
   float scale_log2;       // softmax scale * log2(e)
   int* err;
@@ -220,14 +220,6 @@ __device__ __forceinline__ Unit get_unit(const Params& p, int u, int* err) {
   return x;
 }
 
-// The unit after u of a CTA (warp-collective): round robin, or, where units differ in size, the next one nobody has.
-__device__ __forceinline__ int next_unit(const Params& p, int u) {
-  if (!p.next) return u + (int)gridDim.x;
-  int n = 0;
-  if ((threadIdx.x & 31) == 0) n = (int)gridDim.x + atomicAdd(p.next, 1);
-  return __shfl_sync(0xFFFFFFFFu, n, 0);
-}
-
 // Four codes times their scale as two bf16 pairs, all exact (four significant bits and a power of two): the
 // hardware's e4m3 -> f16 conversion, f32 products, one packing conversion.  Of the ten instructions four are ALU ones;
 // moving the code's bits into a bf16's with integer operations took thirteen, eleven of them ALU, whose
@@ -314,8 +306,8 @@ __device__ __forceinline__ void store_o(const Params& p, const Unit& x, uint32_t
   }
 }
 
-// Chunks over bf16 rows on CTA pairs (mla_pair.cu): tensor maps of the queries (128-row boxes), the rows one by one and
-// whole pages.
+// The kernel on CTA pairs (mla_pair.cu), for every source: tensor maps of the queries (128-row boxes) and, of bf16 rows, of
+// the rows one by one and of whole pages.
 template <Source kSrc>
 cudaError_t launch_pair(const Params& p, const CUtensorMap& qmap, const CUtensorMap& rmap, const CUtensorMap& pmap, int num_sms,
                         cudaStream_t s);

@@ -10,8 +10,8 @@
 // of a tile.  (Sparse attention: one query per tile, its keys are its own.)
 //
 // The pair.  O of 128 rows x 512 values in f32 fills tensor memory, so the values are split over two CTAs; if each
-// computed S = Q K^T for itself, 576 of 1088 multiplications would be done twice (measured: 1.48 ms for 512 tokens x
-// 64 heads at 16k context, against 1.15 ms for the first form of this kernel and 1.10 ms now).  Here the two are a cluster: of every 128 keys (a step) each computes S and
+// computed S = Q K^T for itself, 576 of 1088 multiplications would be done twice (measured, single calls after a pause:
+// 1.48 ms for 512 tokens x 64 heads at 16k context, against 1.15 ms for the first form of this kernel and 1.10 ms now).  Here the two are a cluster: of every 128 keys (a step) each computes S and
 // P for its own 64-key page, and copies P to the other through distributed shared memory (16 KB a step); both multiply
 // the whole P (128 rows x 128 keys) with their half of the values.  Softmax bases have to agree: the rows' maxima of the
 // two pages are exchanged first (one f32 a row).
@@ -21,9 +21,10 @@
 // What bounds it: over bf16 rows (~4000 cycles a step) the shared-memory port, busy for ~2800 of them with the copies in,
 // the products' operands and P, and the exchange between the CTAs; over quantised rows (~6000) the warps that turn codes
 // into bf16.  And the instruction cache: the roles' loops together have to fit it, so most are kept rolled up.
-// Measured: 512 tokens x 64 heads at 16k context 1.10 ms (1080 TFLOP/s); a prompt of 2048 tokens x 128 heads 0.65 ms (900);
-// 64 queries x 128 heads over 2048 selected quantised rows each 74 us (490), 1024 queries x 64 heads 0.80 ms (365: 64
-// heads fill half a tile).
+// Measured, calls back to back: 512 tokens x 64 heads at 16k context 1.22 ms (972 TFLOP/s), a prompt of 2048 tokens x 128
+// heads 0.72 ms (806); both run against the power limit then (single calls after a pause took 1.10 and 0.65 ms).  64 queries
+// x 128 heads over 2048 selected quantised rows each 74 us (491), 1024 queries x 64 heads 0.80 ms (366: 64 heads fill half a
+// tile).
 //
 // Tensor memory: O_v [0, 256), S [256, 320), six of Q's nine column blocks [320, 512).  Shared memory: the other
 // three (48 KB), P of both pages (32 KB), blocks X (16 KB) and Y (24 KB) of the own page, needed until Q K^T is past
@@ -705,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 64; c += 2) {
           const float2 e = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, ns2);
           const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-          // (the normaliser sums the weights before their rounding to bf16, which P V needs)
+          // P is rounded to bf16 (2^-8 of each weight): both operands of a product have one type, and V is bf16.  The
+          // normaliser sums the weights before that.
           ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], w);
           const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
           pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b);
