@@ -185,15 +185,17 @@ class PagedCache:
         data, scale = self.data, self.scale
         nb, bs, dim = data.shape
         dtype = _dtype_code(data)
-        if self._quantised_latent():
-            if dim != LATENT_E4M3_BYTES:
-                raise ValueError("a quantised latent cache has data [num_blocks, 64, 640] uint8")
-            if scale.dtype != torch.float32 or scale.shape != (nb, bs, 4):
-                raise ValueError("a quantised latent cache has scale [num_blocks, 64, 4] float32")
-            dim, dtype = LATENT_E4M3_DIM, DSA_LATENT_E4M3
-        elif dtype == DSA_E4M3 and scale is not None and (scale.dtype != torch.float32 or scale.numel() < nb * bs):
-            # the calls read, and an append writes, one f32 per row through it
-            raise ValueError("an e4m3 cache has scale [num_blocks, block_size] float32")
+        if dtype == DSA_E4M3 and scale is not None:
+            shape = scale.shape
+            if len(shape) == 3 and shape[2] != 1:
+                if dim != LATENT_E4M3_BYTES:
+                    raise ValueError("a quantised latent cache has data [num_blocks, 64, 640] uint8")
+                if scale.dtype is not torch.float32 or shape != (nb, bs, 4):
+                    raise ValueError("a quantised latent cache has scale [num_blocks, 64, 4] float32")
+                dim, dtype = LATENT_E4M3_DIM, DSA_LATENT_E4M3
+            elif scale.dtype is not torch.float32 or scale.numel() < nb * bs:
+                # the calls read, and an append writes, one f32 per row through it
+                raise ValueError("an e4m3 cache has scale [num_blocks, block_size] float32")
         return _PagedCache(_dev_ptr(data, "cache data"), _dev_ptr(scale, "cache scale"), nb, bs, dim, dtype, 0)
 
 
