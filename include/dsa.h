@@ -309,7 +309,8 @@ dsa_status dsa_cache_read(const dsa_paged_cache* cache, const dsa_chunks* chunks
  * A row of the cache that holds infinities or NaN reaches only the tokens that see it (their results are
  * NaN, or what the formula gives for an infinity).  A block id
  * outside the pool sets DSA_DEVERR_BLOCK_ID, a quantised row with a bad scale DSA_DEVERR_SCALE; the
- * row is skipped.  A token all of whose rows are skipped gets out = 0, lse = -inf.
+ * row is skipped.  A token all of whose rows are skipped, or have a logit of -inf, gets out = 0,
+ * lse = -inf.
  * Tensor cores: H <= 1024, d_v == 512, d_rope == 64, bf16 q and 16-byte aligned q and out.
  */
 dsa_status dsa_chunk_mla(const void* q, int32_t q_dtype, int32_t H, int32_t d_v, int32_t d_rope,
