@@ -311,3 +311,73 @@ def test_calls_behind_each_other_see_what_the_last_one_wrote(heads):
             close(some[i:i + 1], o, to, "selected")
             close(lse2[i:i + 1], l, tl, "lse, selected")
     no_error()
+
+
+# ------------------------------------------------------------------------------------------ calls the documentation allows
+
+
+@pytest.mark.parametrize("dim", [1, 7, 64, 100, 200, 256])
+@pytest.mark.parametrize("kind", ["e4m3", "bf16", "f32"])
+@pytest.mark.parametrize("x_dtype", [torch.bfloat16, torch.float32])
+def test_keys_of_other_widths(dim, kind, x_dtype):
+    reqs = Requests([0, 63, 100], [5, 70, 1], seed=90 + dim, pad=2)
+    k = (randn(reqs, reqs.tokens, dim) * torch.exp(4 * randn(reqs, reqs.tokens, 1))).to(x_dtype)
+    dt = {"e4m3": torch.uint8, "bf16": torch.bfloat16, "f32": torch.float32}[kind]
+    keys = dsa.PagedCache(torch.zeros(reqs.num_blocks, 64, dim, dtype=dt, device="cuda"),
+                          torch.ones(reqs.num_blocks, 64, device="cuda") if kind == "e4m3" else None)
+    dsa.dsa_cache_append(k, None, keys, None, reqs.chunks())
+    back = torch.full((reqs.tokens, dim), 7.0, device="cuda")
+    dsa.dsa_cache_read(keys, reqs.chunks(), back)
+    no_error()
+    n = reqs.total
+    if kind == "e4m3":
+        v, s = quantise(k[:n], dim)
+        want = v * s
+    else:
+        want = k[:n].to(dt).double()
+    assert torch.equal(back[:n].double(), want) and bool((back[n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", ["q", "bf16"])
+@pytest.mark.parametrize("heads", [3, 200, 1024])
+def test_chunk_rows_in_front_empty_requests_and_a_loose_bound(kind, heads):
+    # rows before the first request belong to none; requests without tokens anywhere; max_context above every length
+    reqs = Requests([70, 5, 0, 200], [0, 3, 9, 0], seed=91, pad=1)
+    cache, values = make_latent(kind, reqs)
+    table = torch.full((4, 20), -1, dtype=torch.int32, device="cuda")
+    table[:, :reqs.table.shape[1]] = reqs.table
+    lead, T = 2, reqs.tokens + 2
+    q = randn(reqs, T, heads, 576, dtype=torch.bfloat16)
+    out, lse = torch.full((T, heads, 512), 7.0, dtype=q.dtype, device="cuda"), torch.full((T, heads), 7.0, device="cuda")
+    size = dsa.dsa_chunk_mla_workspace_size(T, 4, heads, 512, 1280)
+    ws = torch.full((max(size, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    dsa.dsa_chunk_mla(q, cache, dsa.Chunks(reqs.cu + lead, reqs.seq, table, 1280), TAU, out, lse, ws)
+    no_error()
+    check_chunk(reqs, q[lead:], cache, values, TAU, out[lead:], lse[lead:], kind)
+    for x in (out, lse):
+        assert bool((x[:lead] == 7.0).all()) and bool((x[lead + reqs.total:] == 7.0).all())
+
+
+@pytest.mark.parametrize("heads", [7, 64, 128])
+@pytest.mark.parametrize("k", [1, 37, 300])
+@pytest.mark.parametrize("entry", ["prefill", "decode"])
+def test_sparse_selections_in_any_order_with_repeats(heads, k, entry):
+    # a position selected twice counts twice; -1 may stand anywhere
+    reqs = Requests([0, 400], [3, 4], seed=92)
+    cache, values = make_latent("q", reqs)
+    q = randn(reqs, reqs.total, heads, 576, dtype=torch.bfloat16)
+    g = torch.Generator().manual_seed(k)
+    idx = torch.stack([torch.randint(0, p + 1, (k,), generator=g) for p in reqs.pos]).to(torch.int32)
+    idx[torch.rand(idx.shape, generator=g) < 0.3] = -1
+    idx = idx.cuda()
+    out, lse = sparse(reqs, q, cache, idx, entry=entry)
+    no_error()
+    for t in range(reqs.total):
+        at = idx[t][idx[t] >= 0].long()
+        if not at.numel():
+            assert bool((out[t] == 0).all()) and bool((lse[t] == -math.inf).all())
+            continue
+        v = values[reqs.rows(reqs.req[t])[at]]
+        o, l, to, tl = attend(q[t:t + 1], v, 512, TAU, torch.tensor([at.numel()], device="cuda"), "q")
+        close(out[t:t + 1], o, to, "out")
+        close(lse[t:t + 1], l, tl, "lse")
